@@ -495,6 +495,140 @@ xmoe_status xmoe_ep_recv_plan(const int32_t *recv_counts, int32_t G, int32_t E_l
 xmoe_status xmoe_scatter_rows(const void *src, xmoe_dtype dtype, int64_t n, int32_t d, const int32_t *index,
                               int64_t dst_rows, void *dst, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Around the layer: the pre-norm in front of the gate and the experts, the
+ * gate's balance loss, and the experts' FFN on 8-bit rows.
+ *
+ * xmoe_add_rmsnorm: residual addition and root-mean-square norm,
+ *   sum  = x + res            rounded to the dtype (res NULL: sum = x)
+ *   rstd = 1 / sqrt(mean_c(sum^2) + eps)                       (fp32 [T])
+ *   y    = sum * rstd * gamma                                  (gamma [d])
+ * x, res, sum, y [T,d] and gamma [d] in the dtype.  The norm is that of the
+ * stored (rounded) sum, which is what the backward reads.  res, sum and rstd
+ * may be NULL; y, q or both are required.  q (e4m3 [T,d]) with scale is y in 8
+ * bits (see xmoe_mx8_quantize), quantized from the fp32 values: one rounding.
+ * sum or y may be the buffer of x or of res.  Each row is read and written
+ * once.  Non-finite inputs: an infinity or a NaN in a row makes NaNs of its y.
+ * Limits: d % 8 == 0 (q: % 32 == 0), d <= 16384, T * max(d, 512) < 2^34,
+ * eps >= 0.
+ */
+xmoe_status xmoe_add_rmsnorm(const void *x, const void *res, const void *gamma, xmoe_dtype dtype, int64_t T,
+                             int32_t d, float eps, void *sum, void *y, void *q, void *scale, float *rstd,
+                             void *stream);
+
+/*
+ * Its backward, n = sum * rstd, u = dy * gamma:
+ *   dx     = rstd * (u - n * mean_c(u * n)) (+ dsum)         (dx [T,d], dtype)
+ *   dgamma = sum_t dy * n                                    (fp32 [d])
+ * dx is the gradient of x and of res.  dsum [T,d] (or NULL) is the gradient
+ * that reaches sum on the residual path.  dx may be the buffer of dy, dsum or
+ * sum.  workspace: device, 16-byte aligned,
+ * >= xmoe_add_rmsnorm_bwd_workspace_size bytes, no initialisation needed, dead
+ * after the call.  Fixed-order sums.  T = 0 writes dgamma = 0.  Limits as above.
+ */
+size_t xmoe_add_rmsnorm_bwd_workspace_size(int64_t T, int32_t d, xmoe_dtype dtype);
+xmoe_status xmoe_add_rmsnorm_bwd(const void *dy, const void *dsum, const void *sum, const void *gamma,
+                                 const float *rstd, xmoe_dtype dtype, int64_t T, int32_t d, void *dx,
+                                 float *dgamma, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * xmoe_balance_loss: the gate's load-balance loss and per-expert counts, from
+ * what xmoe_route wrote.  Tokens are counted by sequence: sequence s holds the
+ * tokens [seq_offsets[s], seq_offsets[s+1]) (DEVICE int32 [n_seq+1],
+ * non-decreasing; NULL: one sequence of all T tokens).  Tokens in front of the
+ * first or behind the last sequence, and tokens whose token_mask byte is 0
+ * (DEVICE uint8 [T], or NULL), do not count.  With p = softmax(logits[t]), n_s
+ * counted tokens and S' sequences that count any:
+ *   counts[s,e] = slots of counted tokens of s with topk_ids == e     (int32)
+ *   loss        = alpha / S' * sum_s sum_e (E counts[s,e] / (k n_s)) * mean_t p[t,e]
+ *   coef[s,e]   = d loss / d p[t,e] = alpha E counts[s,e] / (k n_s^2 S')
+ * loss fp32 [1]; counts, coef [n_seq,E].  A sequence that counts nothing has
+ * zeros; if none does, loss is 0.  Ids outside [0,E) are not counted.  The
+ * counts carry no gradient.  logits fp32 [T,E], 16-byte aligned; a row may hold
+ * -infinity in places, not everywhere.  workspace: device, 16-byte aligned,
+ * >= xmoe_balance_loss_workspace_size bytes, no initialisation needed, dead
+ * after the call (concurrent calls need one each).
+ * Limits: 1 <= k <= E <= 1024, T <= 2^26, 1 <= n_seq <= 4096.
+ */
+size_t xmoe_balance_loss_workspace_size(int64_t T, int32_t E, int32_t n_seq);
+xmoe_status xmoe_balance_loss(const float *logits, const int32_t *topk_ids, int64_t T, int32_t E, int32_t k,
+                              const int32_t *seq_offsets, int32_t n_seq, const uint8_t *token_mask, float alpha,
+                              float *loss, int32_t *counts, float *coef, void *workspace, size_t ws_bytes,
+                              void *stream);
+
+/*
+ * Gradient of the loss with respect to the logits, g = *dloss (DEVICE fp32
+ * scalar; NULL: 1):
+ *   dlogits[t,e] = g p[t,e] (coef[s,e] - sum_e' p[t,e'] coef[s,e'])
+ * and 0 for tokens that do not count, whatever their logits hold (fp32 [T,E],
+ * 16-byte aligned).
+ */
+xmoe_status xmoe_balance_loss_bwd(const float *logits, const float *coef, int64_t T, int32_t E,
+                                  const int32_t *seq_offsets, int32_t n_seq, const uint8_t *token_mask,
+                                  const float *dloss, float *dlogits, void *stream);
+
+/*
+ * xmoe_route_bwd with the balance loss's gradient: g[t,e] there gains
+ * (*dloss) coef[s,e] for every expert of a counted token, so that dx and dwg
+ * hold both gradients and no [T,E] gradient is materialised.  Other arguments,
+ * workspace and limits as xmoe_route_bwd and xmoe_balance_loss.
+ */
+xmoe_status xmoe_route_bwd_balance(const void *x, const void *wg, const float *logits, const int32_t *topk_ids,
+                                   const float *dtopk_w, int32_t ldw, const float *coef,
+                                   const int32_t *seq_offsets, int32_t n_seq, const uint8_t *token_mask,
+                                   const float *dloss, xmoe_dtype dtype, int64_t T, int32_t d, int32_t E, int32_t k,
+                                   float inv_temperature, int32_t accumulate, void *dx, float *dwg, void *workspace,
+                                   size_t ws_bytes, void *stream);
+
+/*
+ * 8-bit rows: q e4m3 [n,K] and a scale byte b, standing for 2^(b - 127), for
+ * each 32 consecutive elements of a row.  b is the least power of two that
+ * brings the block's largest magnitude to at most 448, not below 2^-127;
+ * elements are rounded to nearest even.  An all-zero block has b = 127; a block
+ * that holds an infinity or a NaN has b = 255 and stands for NaNs.  scale is
+ * uint8 [ceil(K/128), n, 4]: byte (g / 4, row, g % 4) belongs to elements
+ * [32 g, 32 g + 32); bytes with 32 g >= K are 127 (written so by every call
+ * here, and required to be finite, not 255, by those that read them).
+ *   xmoe_mx8_quantize:   x [n,K] (dtype) -> q, scale
+ *   xmoe_mx8_dequantize: q, scale -> out [n,K] (dtype), exact where the dtype's
+ *                        exponent range holds the value
+ *   xmoe_mx8_quantize_weights: w [E,K,N] (dtype, the layer's layout) -> q
+ *                        [E,N,K], scale [E, ceil(K/128), N, 4], the summed axis
+ *                        last; once per weight update.
+ * Limits: K (and N) multiples of 32, at most 65536; n * max(K, 512) < 2^34;
+ * E <= 1024, E * ceil(K/128) * ceil(N/64) < 2^24.  All arrays 16-byte aligned.
+ */
+xmoe_status xmoe_mx8_quantize(const void *x, xmoe_dtype dtype, int64_t n, int32_t K, void *q, void *scale,
+                              void *stream);
+xmoe_status xmoe_mx8_dequantize(const void *q, const void *scale, xmoe_dtype dtype, int64_t n, int32_t K, void *out,
+                                void *stream);
+xmoe_status xmoe_mx8_quantize_weights(const void *w, xmoe_dtype dtype, int32_t E, int32_t K, int32_t N, void *q,
+                                      void *scale, void *stream);
+
+/*
+ * The experts' FFN on 8-bit rows and weights, for serving (no backward):
+ *   up   : H1 = x[r] . w1[e], H3 = x[r] . w3[e];  act[r] = silu(H1) * H3 in 8 bits
+ *   down : ye[r] = act[r] . w2[e]                          (bf16 [rows,d])
+ * for the rows r of expert e, the products of the values that the 8-bit
+ * operands stand for, summed in fp32; act is quantized from fp32.
+ * xq, xscale: 8-bit rows [T,d]; row r of the experts' rows is row token_ids[r]
+ * of them (DEVICE int32 [rows]; ids outside [0,T) read a row of zeros), or row
+ * r itself with token_ids NULL (then T == rows).  w1, w3 [E,h,d] and w2 [E,d,h]
+ * with their scales as xmoe_mx8_quantize_weights lays them out (from the
+ * layer's [E,d,h] and [E,h,d]).  act [rows,h], act_scale [ceil(h/128),rows,4].
+ * expert_offsets as xmoe_expert_ffn_up; rows outside every segment are left as
+ * they were.  Deterministic.  A NaN in a row's block makes NaNs of that row.
+ * Limits: d, h multiples of 32, at most 65536; E <= 1024; rows * max(d, h, 512)
+ * < 2^34; T * d < 2^31 with token_ids.
+ */
+xmoe_status xmoe_expert_ffn_up_mx8(const void *xq, const void *xscale, const int32_t *token_ids, int64_t T,
+                                   const void *w1, const void *w1_scale, const void *w3, const void *w3_scale,
+                                   const int32_t *expert_offsets, int32_t E, int64_t rows, int32_t d, int32_t h,
+                                   void *act, void *act_scale, void *stream);
+xmoe_status xmoe_expert_ffn_down_mx8(const void *act, const void *act_scale, const void *w2, const void *w2_scale,
+                                     const int32_t *expert_offsets, int32_t E, int64_t rows, int32_t d, int32_t h,
+                                     void *ye, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,6 +8,7 @@ CPU or PyTorch fallback: if the library is missing the import fails.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -25,6 +26,10 @@ __all__ = [
     "xmoe_expert_ffn_bwd_dw2", "xmoe_dispatch_bwd", "xmoe_route_bwd_workspace_size", "xmoe_route_bwd",
     "xmoe_build_pilots_workspace_size", "xmoe_build_pilots", "xmoe_ep_send_plan", "xmoe_ep_recv_plan_workspace_size",
     "xmoe_ep_recv_plan", "xmoe_scatter_rows",
+    "xmoe_add_rmsnorm", "xmoe_add_rmsnorm_bwd", "xmoe_add_rmsnorm_bwd_workspace_size",
+    "xmoe_balance_loss", "xmoe_balance_loss_workspace_size", "xmoe_balance_loss_bwd", "xmoe_route_bwd_balance",
+    "mx8_scale_shape", "xmoe_mx8_quantize", "xmoe_mx8_dequantize", "xmoe_mx8_quantize_weights",
+    "xmoe_expert_ffn_up_mx8", "xmoe_expert_ffn_down_mx8",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -102,6 +107,24 @@ _lib_ep_send = _sig("xmoe_ep_send_plan", [_vp, _i32, _i32, _vp, _vp, _vp])
 _lib_ep_recv_ws = _sig("xmoe_ep_recv_plan_workspace_size", [_i32, _i32], _sz)
 _lib_ep_recv = _sig("xmoe_ep_recv_plan", [_vp, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
 _lib_scatter_rows = _sig("xmoe_scatter_rows", [_vp, ctypes.c_int, _i64, _i32, _vp, _i64, _vp, _vp])
+
+_lib_norm = _sig("xmoe_add_rmsnorm", [_vp, _vp, _vp, ctypes.c_int, _i64, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp])
+_lib_norm_bwd_ws = _sig("xmoe_add_rmsnorm_bwd_workspace_size", [_i64, _i32, ctypes.c_int], _sz)
+_lib_norm_bwd = _sig("xmoe_add_rmsnorm_bwd", [_vp, _vp, _vp, _vp, _vp, ctypes.c_int, _i64, _i32, _vp, _vp, _vp, _sz,
+                                              _vp])
+_lib_balance_ws = _sig("xmoe_balance_loss_workspace_size", [_i64, _i32, _i32], _sz)
+_lib_balance = _sig("xmoe_balance_loss", [_vp, _vp, _i64, _i32, _i32, _vp, _i32, _vp, _f32, _vp, _vp, _vp, _vp, _sz,
+                                          _vp])
+_lib_balance_bwd = _sig("xmoe_balance_loss_bwd", [_vp, _vp, _i64, _i32, _vp, _i32, _vp, _vp, _vp, _vp])
+_lib_rbwd_balance = _sig("xmoe_route_bwd_balance", [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp,
+                                                    ctypes.c_int, _i64, _i32, _i32, _i32, _f32, _i32, _vp, _vp, _vp,
+                                                    _sz, _vp])
+_lib_mx8_q = _sig("xmoe_mx8_quantize", [_vp, ctypes.c_int, _i64, _i32, _vp, _vp, _vp])
+_lib_mx8_dq = _sig("xmoe_mx8_dequantize", [_vp, _vp, ctypes.c_int, _i64, _i32, _vp, _vp])
+_lib_mx8_qw = _sig("xmoe_mx8_quantize_weights", [_vp, ctypes.c_int, _i32, _i32, _i32, _vp, _vp, _vp])
+_lib_up8 = _sig("xmoe_expert_ffn_up_mx8", [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp,
+                                           _vp, _vp])
+_lib_down8 = _sig("xmoe_expert_ffn_down_mx8", [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp])
 
 
 class XmoeError(RuntimeError):
@@ -564,3 +587,205 @@ def xmoe_scatter_rows(src, index, dst, n: Optional[int] = None, stream=None):
         raise ValueError("dst must be [rows, d] in src's dtype")
     _check(_lib_scatter_rows(_ptr(src), _dt(src), n, d, _ptr(index), dst.shape[0], _ptr(dst), _stream(stream)),
            "xmoe_scatter_rows")
+
+
+# ------------------------------------------------ around the layer
+
+_F8, _U8 = torch.float8_e4m3fn, torch.uint8
+
+
+def _one_device(*ts: Optional[torch.Tensor]):
+    """Context of the call's device (the library launches on the current one),
+    which all its tensors must share."""
+    ts = [t for t in ts if t is not None]
+    if any(t.device != ts[0].device for t in ts):
+        raise ValueError("the call's tensors are on different devices")
+    dev = ts[0].device
+    if not ts[0].is_cuda or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()  # host tensors are refused when their pointers are taken
+    return torch.cuda.device(dev)
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, like: torch.Tensor):
+    """(tensor, bytes): the caller's workspace, or one of `need` bytes."""
+    if ws is None:
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+    return ws, ws.numel() * ws.element_size()
+
+
+def xmoe_add_rmsnorm(x, res, gamma, eps: float, sum=None, y=None, q=None, scale=None, rstd=None, stream=None):
+    """sum = x + res (res None: x), y = sum * rstd * gamma; with q and scale the
+    same in 8 bits.  sum, y, (q, scale) and rstd are outputs; y or q is required."""
+    T, d = x.shape
+    for t, name in ((res, "res"), (sum, "sum"), (y, "y")):
+        _shape(t, (T, d), name, x.dtype)
+    _shape(gamma, (d,), "gamma", x.dtype)
+    _shape(q, (T, d), "q", _F8)
+    _shape(scale, mx8_scale_shape(T, d), "scale", _U8)
+    _shape(rstd, (T,), "rstd", _F32)
+    with _one_device(x, res, gamma, sum, y, q, scale, rstd):
+        _check(_lib_norm(_ptr(x), _ptr(res), _ptr(gamma), _dt(x), T, d, eps, _ptr(sum), _ptr(y), _ptr(q), _ptr(scale),
+                         _ptr(rstd), _stream(stream)), "xmoe_add_rmsnorm")
+
+
+def xmoe_add_rmsnorm_bwd_workspace_size(T: int, d: int, dtype) -> int:
+    return int(_lib_norm_bwd_ws(T, d, XMOE_BF16 if dtype == torch.bfloat16 else XMOE_F32))
+
+
+def xmoe_add_rmsnorm_bwd(dy, dsum, sum, gamma, rstd, dx, dgamma, workspace=None, stream=None):
+    """dx of x and res from dy (and dsum, the residual path's gradient, or None);
+    dgamma fp32 [d].  workspace: allocated here (torch) when None."""
+    T, d = dy.shape
+    for t, name in ((dsum, "dsum"), (sum, "sum"), (dx, "dx")):
+        _shape(t, (T, d), name, dy.dtype)
+    _shape(gamma, (d,), "gamma", dy.dtype)
+    _shape(rstd, (T,), "rstd", _F32)
+    _shape(dgamma, (d,), "dgamma", _F32)
+    workspace, nbytes = _workspace(workspace, xmoe_add_rmsnorm_bwd_workspace_size(T, d, dy.dtype), dy)
+    with _one_device(dy, dsum, sum, gamma, rstd, dx, dgamma, workspace):
+        _check(_lib_norm_bwd(_ptr(dy), _ptr(dsum), _ptr(sum), _ptr(gamma), _ptr(rstd), _dt(dy), T, d, _ptr(dx),
+                             _ptr(dgamma), _ptr(workspace), nbytes, _stream(stream)), "xmoe_add_rmsnorm_bwd")
+
+
+def _sequences(logits, seq_offsets, token_mask, coef) -> int:
+    T, E = logits.shape
+    if seq_offsets is not None and (seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2):
+        raise ValueError("seq_offsets: [n_seq + 1] with n_seq >= 1")
+    n_seq = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    _shape(logits, (T, E), "logits", _F32)
+    _shape(seq_offsets, (n_seq + 1,), "seq_offsets", _I32)
+    _shape(coef, (n_seq, E), "coef", _F32)
+    _shape(token_mask, (T,), "token_mask")
+    if token_mask is not None and token_mask.dtype not in (torch.bool, _U8):
+        raise TypeError(f"token_mask: dtype {token_mask.dtype}, the call needs bool or uint8")
+    return n_seq
+
+
+def xmoe_balance_loss_workspace_size(T: int, E: int, n_seq: int = 1) -> int:
+    return int(_lib_balance_ws(T, E, n_seq))
+
+
+def xmoe_balance_loss(logits, topk_ids, alpha: float, loss, counts, coef, seq_offsets=None, token_mask=None,
+                      workspace=None, stream=None):
+    """loss [1], counts and coef [n_seq, E] of the gate's balance loss; seq_offsets
+    int32 [n_seq + 1] (None: one sequence), token_mask bool or uint8 [T] (None:
+    all count).  workspace: allocated here (torch) when None."""
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    n_seq = _sequences(logits, seq_offsets, token_mask, coef)
+    _shape(topk_ids, (T, k), "topk_ids", _I32)
+    _shape(loss, (1,), "loss", _F32)
+    _shape(counts, (n_seq, E), "counts", _I32)
+    workspace, nbytes = _workspace(workspace, xmoe_balance_loss_workspace_size(T, E, n_seq), logits)
+    with _one_device(logits, topk_ids, loss, counts, coef, seq_offsets, token_mask, workspace):
+        _check(_lib_balance(_ptr(logits), _ptr(topk_ids), T, E, k, _ptr(seq_offsets), n_seq, _ptr(token_mask), alpha,
+                            _ptr(loss), _ptr(counts), _ptr(coef), _ptr(workspace), nbytes, _stream(stream)),
+               "xmoe_balance_loss")
+
+
+def xmoe_balance_loss_bwd(logits, coef, dlogits, seq_offsets=None, token_mask=None, dloss=None, stream=None):
+    """dlogits [T, E] of the balance loss; dloss: its upstream gradient, fp32 [1]
+    on the device (None: 1)."""
+    T, E = logits.shape
+    n_seq = _sequences(logits, seq_offsets, token_mask, coef)
+    _shape(dlogits, (T, E), "dlogits", _F32)
+    _shape(dloss, (1,), "dloss", _F32)
+    with _one_device(logits, coef, dlogits, seq_offsets, token_mask, dloss):
+        _check(_lib_balance_bwd(_ptr(logits), _ptr(coef), T, E, _ptr(seq_offsets), n_seq, _ptr(token_mask),
+                                _ptr(dloss), _ptr(dlogits), _stream(stream)), "xmoe_balance_loss_bwd")
+
+
+def xmoe_route_bwd_balance(x, wg, logits, topk_ids, dtopk_w, coef, dx, dwg, workspace, inv_temperature: float = 1.0,
+                           accumulate: bool = True, seq_offsets=None, token_mask=None, dloss=None, stream=None):
+    """xmoe_route_bwd with the balance loss's gradient in dx and dwg."""
+    T, d = x.shape
+    E = wg.shape[1]
+    k = topk_ids.shape[1]
+    n_seq = _sequences(logits, seq_offsets, token_mask, coef)
+    _shape(wg, (d, E), "wg", x.dtype)
+    _shape(logits, (T, E), "logits", _F32)
+    _shape(topk_ids, (T, k), "topk_ids", _I32)
+    _shape(dtopk_w, (T, k), "dtopk_w", _F32)
+    if not dtopk_w.is_cuda or dtopk_w.stride(1) != 1:
+        raise ValueError("dtopk_w must be a device tensor with unit column stride")
+    _shape(dx, (T, d), "dx", x.dtype)
+    _shape(dwg, (d, E), "dwg", _F32)
+    _shape(dloss, (1,), "dloss", _F32)
+    with _one_device(x, wg, logits, topk_ids, dtopk_w, coef, dx, dwg, workspace, seq_offsets, token_mask, dloss):
+        _check(_lib_rbwd_balance(_ptr(x), _ptr(wg), _ptr(logits), _ptr(topk_ids), dtopk_w.data_ptr(),
+                                 dtopk_w.stride(0), _ptr(coef),
+                                 _ptr(seq_offsets), n_seq, _ptr(token_mask), _ptr(dloss), _dt(x), T, d, E, k,
+                                 inv_temperature, int(bool(accumulate)), _ptr(dx), _ptr(dwg), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)),
+               "xmoe_route_bwd_balance")
+
+
+def mx8_scale_shape(n: int, K: int):
+    """Shape of the scale bytes of n 8-bit rows of K elements."""
+    return ((K + 127) // 128, n, 4)
+
+
+def xmoe_mx8_quantize(x, q, scale, stream=None):
+    """x [n, K] -> q float8_e4m3fn [n, K], scale uint8 mx8_scale_shape(n, K)."""
+    n, K = x.shape
+    _shape(q, (n, K), "q", _F8)
+    _shape(scale, mx8_scale_shape(n, K), "scale", _U8)
+    with _one_device(x, q, scale):
+        _check(_lib_mx8_q(_ptr(x), _dt(x), n, K, _ptr(q), _ptr(scale), _stream(stream)), "xmoe_mx8_quantize")
+
+
+def xmoe_mx8_dequantize(q, scale, out, stream=None):
+    """The values of 8-bit rows, in out's dtype."""
+    n, K = out.shape
+    _shape(q, (n, K), "q", _F8)
+    _shape(scale, mx8_scale_shape(n, K), "scale", _U8)
+    with _one_device(q, scale, out):
+        _check(_lib_mx8_dq(_ptr(q), _ptr(scale), _dt(out), n, K, _ptr(out), _stream(stream)), "xmoe_mx8_dequantize")
+
+
+def xmoe_mx8_quantize_weights(w, q, scale, stream=None):
+    """w [E, K, N] (the layer's layout) -> q float8_e4m3fn [E, N, K], scale uint8
+    [E, *mx8_scale_shape(N, K)]."""
+    E, K, N = w.shape
+    _shape(q, (E, N, K), "q", _F8)
+    _shape(scale, (E,) + mx8_scale_shape(N, K), "scale", _U8)
+    with _one_device(w, q, scale):
+        _check(_lib_mx8_qw(_ptr(w), _dt(w), E, K, N, _ptr(q), _ptr(scale), _stream(stream)),
+               "xmoe_mx8_quantize_weights")
+
+
+def xmoe_expert_ffn_up_mx8(xq, xscale, w1, w1_scale, w3, w3_scale, expert_offsets, act, act_scale, token_ids=None,
+                           stream=None):
+    """act, act_scale = 8-bit silu(x . w1) * (x . w3) over each expert's rows; row r
+    is row token_ids[r] of xq (None: row r)."""
+    T, d = xq.shape
+    E, h, _ = w1.shape
+    rows = act.shape[0]
+    _shape(xq, (T, d), "xq", _F8)
+    _shape(xscale, mx8_scale_shape(T, d), "xscale", _U8)
+    for t, s, name in ((w1, w1_scale, "w1"), (w3, w3_scale, "w3")):
+        _shape(t, (E, h, d), name, _F8)
+        _shape(s, (E,) + mx8_scale_shape(h, d), name + "_scale", _U8)
+    _shape(expert_offsets, (E + 1,), "expert_offsets", _I32)
+    _shape(act, (rows, h), "act", _F8)
+    _shape(act_scale, mx8_scale_shape(rows, h), "act_scale", _U8)
+    _shape(token_ids, (rows,), "token_ids", _I32)
+    with _one_device(xq, xscale, w1, w1_scale, w3, w3_scale, expert_offsets, act, act_scale, token_ids):
+        _check(_lib_up8(_ptr(xq), _ptr(xscale), _ptr(token_ids), T, _ptr(w1), _ptr(w1_scale), _ptr(w3),
+                        _ptr(w3_scale), _ptr(expert_offsets), E, rows, d, h, _ptr(act), _ptr(act_scale),
+                        _stream(stream)), "xmoe_expert_ffn_up_mx8")
+
+
+def xmoe_expert_ffn_down_mx8(act, act_scale, w2, w2_scale, expert_offsets, ye, stream=None):
+    """ye [rows, d] (bf16) = act . w2 over each expert's rows."""
+    rows, h = act.shape
+    E, d, _ = w2.shape
+    _shape(act, (rows, h), "act", _F8)
+    _shape(act_scale, mx8_scale_shape(rows, h), "act_scale", _U8)
+    _shape(w2, (E, d, h), "w2", _F8)
+    _shape(w2_scale, (E,) + mx8_scale_shape(d, h), "w2_scale", _U8)
+    _shape(expert_offsets, (E + 1,), "expert_offsets", _I32)
+    _shape(ye, (rows, d), "ye", torch.bfloat16)
+    with _one_device(act, act_scale, w2, w2_scale, expert_offsets, ye):
+        _check(_lib_down8(_ptr(act), _ptr(act_scale), _ptr(w2), _ptr(w2_scale), _ptr(expert_offsets), E, rows, d, h,
+                          _ptr(ye), _stream(stream)), "xmoe_expert_ffn_down_mx8")

@@ -9,12 +9,14 @@
 #include <mutex>
 #include <string>
 
-#include "../../include/xmoe.h"
+#include "api_common.hpp"
 #include "kernels.hpp"
 
 namespace {
-
 thread_local std::string g_err;
+}
+
+namespace xmoe_api {
 
 xmoe_status fail(xmoe_status st, const char *fmt, ...) {
     char buf[512];
@@ -37,9 +39,11 @@ xmoe_status hip_status(hipError_t e, const char *what) {
 }
 
 // Architecture check of the current device, cached per device ordinal.
+namespace {
 constexpr int kMaxDevices = 64;
 int g_arch[kMaxDevices];  // 0 unknown, 1 gfx950, 2 other
 std::mutex g_arch_mu;
+}  // namespace
 
 xmoe_status check_device() {
     int dev = 0;
@@ -58,29 +62,16 @@ xmoe_status check_device() {
     return XMOE_OK;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-#define REQUIRE(cond, st, ...)                  \
-    do {                                        \
-        if (!(cond)) return fail(st, __VA_ARGS__); \
-    } while (0)
-
-#define CHECK_DEVICE()                          \
-    do {                                        \
-        xmoe_status _s = check_device();        \
-        if (_s != XMOE_OK) return _s;           \
-    } while (0)
-
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
-
-// a * b <= limit for a, b >= 0, without forming a product that could overflow
-// (callers may pass any int64 size; the checks must stay defined for all)
-bool within(int64_t a, int64_t b, int64_t limit) { return a >= 0 && b >= 0 && (b == 0 || a <= limit / b); }
-
 xmoe_status check_dtype(xmoe_dtype dt) {
     if (dt != XMOE_F32 && dt != XMOE_BF16) return fail(XMOE_ERR_UNSUPPORTED, "unknown dtype %d", static_cast<int>(dt));
     return XMOE_OK;
 }
+
+}  // namespace xmoe_api
+
+using namespace xmoe_api;
+
+namespace {
 
 xmoe_status check_pft(const xmoe_pft *pft, bool need_s2r, bool need_w, bool need_all) {
     if (!pft) return fail(XMOE_ERR_INVALID_VALUE, "pft is NULL");
@@ -123,14 +114,6 @@ xmoe_status check_grad_dt(xmoe_dtype dtype, xmoe_dtype grad_dt, int32_t accumula
         return fail(XMOE_ERR_UNSUPPORTED, "accumulating weight gradients needs grad_dt = XMOE_F32");
     return XMOE_OK;
 }
-
-#define TRY(expr)                         \
-    do {                                  \
-        xmoe_status _s = (expr);          \
-        if (_s != XMOE_OK) return _s;     \
-    } while (0)
-
-inline hipStream_t S(void *s) { return static_cast<hipStream_t>(s); }
 
 xmoe::PftPtrs to_ptrs(const xmoe_pft *p) {
     return {p->token_ids, p->expert_ids, p->tokens_per_expert, p->expert_offsets, p->combine_weights, p->slot_to_row};

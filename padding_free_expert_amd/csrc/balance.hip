@@ -1,0 +1,366 @@
+// Balance loss of the gate: per-expert counts, loss and gradient.
+//
+// For sequence s with n_s counted tokens, c_{s,e} of whose slots chose expert e,
+// and p = softmax(logits) (the gate's probabilities):
+//   f_{s,e} = E c_{s,e} / (k n_s),  P_{s,e} = (1 / n_s) sum_t p_{t,e}
+//   loss = alpha / S' * sum_s sum_e f_{s,e} P_{s,e}
+// over the S' sequences that count any token.  The counts carry no gradient, so
+//   coef_{s,e} = d loss / d p_{t,e} = alpha E c_{s,e} / (k n_s^2 S')
+//   d loss / d logits_{t,e} = p_{t,e} (coef_{s,e} - sum_e' p_{t,e'} coef_{s,e'})
+//
+// Forward: one kernel reads the logits once; a block forms the probabilities of
+// a chunk of tokens and the sums and counts of each sequence's piece of it.
+// Piece (chunk b, sequence s) has row b + s of the partial sums: chunks and
+// sequences both only go forward, so no two pieces share a row and the rows
+// number at most chunks + S.  A second kernel, one block per sequence, adds a
+// sequence's rows in order and writes counts and coef; its last block to end
+// adds the sequences' losses in order.  Nothing depends on the order in which
+// blocks run.  Memory-bound: the logits are read once here, once in the
+// backward, which writes the gradient.
+#include <algorithm>
+
+#include "balance.hpp"
+#include "common.hpp"
+#include "kernels.hpp"
+
+namespace xmoe {
+
+namespace {
+
+constexpr int kWaves = 4;
+
+// Tokens per block: about 512 blocks, at least one step of every wave
+inline int chunk_tokens(int64_t T) {
+    int c = 16;
+    while (c < 128 && T > static_cast<int64_t>(c) * 512) c *= 2;
+    return c;
+}
+inline size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+struct BalanceWs {
+    float *psum;      // [rows, E]
+    int32_t *csum;    // [rows, E]
+    int32_t *nsum;    // [rows]
+    double *seq_loss; // [S]
+    int32_t *ticket;  // [1]
+    size_t bytes;
+};
+BalanceWs balance_ws(void *ws, int64_t T, int E, int S) {
+    const int64_t rows = (T + chunk_tokens(T) - 1) / chunk_tokens(T) + S;
+    BalanceWs b;
+    size_t at = 0;
+    char *p = static_cast<char *>(ws);
+    auto take = [&](size_t n) {
+        char *q = p + at;
+        at += align256(n);
+        return q;
+    };
+    b.psum = reinterpret_cast<float *>(take(rows * E * 4));
+    b.csum = reinterpret_cast<int32_t *>(take(rows * E * 4));
+    b.nsum = reinterpret_cast<int32_t *>(take(rows * 4));
+    b.seq_loss = reinterpret_cast<double *>(take(static_cast<size_t>(S) * 8));
+    b.ticket = reinterpret_cast<int32_t *>(take(4));
+    b.bytes = at;
+    return b;
+}
+
+// Probabilities of one token in its LT lanes: lane r holds QQ experts, the
+// 16-byte chunks r, r + LT, ... of the row (expert of value q: 4 (r + LT (q / 4))
+// + q % 4).  Experts past E and dead tokens hold 0.
+template <int LT, int QQ>
+__device__ __forceinline__ void token_softmax(const float *row, bool live, int r, int E, float (&p)[QQ]) {
+    auto ex = [&](int q) { return 4 * (r + LT * (q >> 2)) + (q & 3); };
+#pragma unroll
+    for (int q = 0; q < QQ; ++q) p[q] = -INFINITY;
+    if (live) {
+        if (E % 4 == 0) {
+#pragma unroll
+            for (int q = 0; q < QQ; q += 4)
+                if (ex(q) < E) {
+                    const float4 v = *reinterpret_cast<const float4 *>(row + ex(q));
+                    p[q] = v.x; p[q + 1] = v.y; p[q + 2] = v.z; p[q + 3] = v.w;
+                }
+        } else {
+#pragma unroll
+            for (int q = 0; q < QQ; ++q)
+                if (ex(q) < E) p[q] = row[ex(q)];
+        }
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < QQ; ++q) mx = fmaxf(mx, p[q]);
+#pragma unroll
+    for (int off = LT / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+    float den = 0.0f;
+#pragma unroll
+    for (int q = 0; q < QQ; ++q) {
+        p[q] = ex(q) < E && live ? expf(p[q] - mx) : 0.0f;
+        den += p[q];
+    }
+#pragma unroll
+    for (int off = LT / 2; off > 0; off >>= 1) den += __shfl_xor(den, off, 64);
+#pragma unroll
+    for (int q = 0; q < QQ; ++q) p[q] = live ? p[q] / den : 0.0f;
+}
+
+template <int LT, int QQ>
+__global__ __launch_bounds__(64 * kWaves) void balance_part_kernel(const float *__restrict__ logits,
+                                                                   const int32_t *__restrict__ ids, int64_t T, int E,
+                                                                   int k, const int32_t *__restrict__ off, int S,
+                                                                   const uint8_t *__restrict__ mask, int chunk,
+                                                                   BalanceWs ws) {
+    constexpr int TPW = 64 / LT, TPB = kWaves * TPW;
+    __shared__ float sp[kWaves][LT * QQ];
+    __shared__ int32_t sc[LT * QQ];
+    __shared__ int32_t sn[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane % LT, slot = wave * TPW + lane / LT;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
+    const int64_t t1 = t0 + chunk < T ? t0 + chunk : T;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *ws.ticket = 0;
+    auto ex = [&](int q) { return 4 * (r + LT * (q >> 2)) + (q & 3); };
+    // the sequences that this chunk meets, in order (the same in every thread)
+    int s = 0;
+    if (off) s = max(find_sequence<64>(off, S, t0), 0);
+    for (; s < S; ++s) {
+        int64_t lo = 0, hi = T;
+        if (off) {
+            lo = off[s];
+            hi = off[s + 1];
+            if (lo >= t1) break;
+        }
+        lo = lo < t0 ? t0 : lo;
+        hi = hi > t1 ? t1 : hi;
+        if (lo >= hi) continue;  // an empty sequence: no row
+        for (int e = threadIdx.x; e < LT * QQ; e += 64 * kWaves) sc[e] = 0;
+        float acc[QQ];
+        int n = 0;
+#pragma unroll
+        for (int q = 0; q < QQ; ++q) acc[q] = 0.0f;
+        __syncthreads();
+        for (int64_t tb = lo; tb < hi; tb += TPB) {
+            const int64_t t = tb + slot;
+            const bool live = t < hi && (!mask || mask[t] != 0);
+            float p[QQ];
+            token_softmax<LT, QQ>(logits + t * E, live, r, E, p);
+#pragma unroll
+            for (int q = 0; q < QQ; ++q) acc[q] += p[q];
+            if (live) {
+                n += r == 0 ? 1 : 0;
+                for (int j = r; j < k; j += LT) {
+                    const int e = ids[t * k + j];
+                    if (e >= 0 && e < E) atomicAdd(&sc[e], 1);
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < QQ; ++q)
+#pragma unroll
+            for (int o = LT; o < 64; o <<= 1) acc[q] += __shfl_xor(acc[q], o, 64);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, 64);
+        if (lane < LT) {
+#pragma unroll
+            for (int q = 0; q < QQ; ++q) sp[wave][ex(q)] = acc[q];
+        }
+        if (lane == 0) sn[wave] = n;
+        __syncthreads();
+        const int64_t row = static_cast<int64_t>(blockIdx.x) + s;
+        for (int e = threadIdx.x; e < E; e += 64 * kWaves) {
+            float v = sp[0][e];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) v += sp[w][e];
+            ws.psum[row * E + e] = v;
+            ws.csum[row * E + e] = sc[e];
+        }
+        if (threadIdx.x == 0) {
+            int v = sn[0];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) v += sn[w];
+            ws.nsum[row] = v;
+        }
+        __syncthreads();
+    }
+}
+
+// the rows [lo, hi) of sequence s in the partial sums
+__device__ __forceinline__ void piece_rows(const int32_t *off, int s, int64_t T, int chunk, int64_t *lo, int64_t *hi) {
+    int64_t a = 0, b = T;
+    if (off) {
+        a = off[s];
+        b = off[s + 1];
+    }
+    a = a < 0 ? 0 : a;
+    b = b > T ? T : b;
+    *lo = a < b ? a / chunk + s : 0;
+    *hi = a < b ? (b - 1) / chunk + s + 1 : 0;
+}
+
+template <typename V>
+__device__ __forceinline__ V block_sum(V v, V *red) {  // 1024 threads, fixed order
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < 16; ++w) v += red[w];
+    return v;
+}
+
+__global__ __launch_bounds__(1024) void balance_final_kernel(int64_t T, int E, int k, const int32_t *off, int S,
+                                                             int chunk, float alpha, BalanceWs ws, float *loss,
+                                                             int32_t *counts, float *coef) {
+    __shared__ double red[16];
+    __shared__ int32_t redi[16];
+    __shared__ double sp[1024];
+    __shared__ int32_t sc[1024];
+    __shared__ int last;
+    const int s = blockIdx.x;
+    int64_t lo, hi;
+    // S': sequences that count a token.  A sequence's first piece mostly tells.
+    int some = 0;
+    for (int i = threadIdx.x; i < S; i += 1024) {
+        piece_rows(off, i, T, chunk, &lo, &hi);
+        int any = 0;
+        for (int64_t b = lo; b < hi && !any; ++b) any = ws.nsum[b] > 0;
+        some += any;
+    }
+    some = block_sum(some, redi);
+    piece_rows(off, s, T, chunk, &lo, &hi);
+    int n = 0;
+    for (int64_t b = lo + threadIdx.x; b < hi; b += 1024) n += ws.nsum[b];
+    n = block_sum(n, redi);
+    // an expert per lane, the rest of the block shares the rows
+    const int width = E <= 64 ? 64 : E <= 128 ? 128 : E <= 256 ? 256 : E <= 512 ? 512 : 1024;
+    const int e = threadIdx.x & (width - 1), part = threadIdx.x / width, parts = 1024 / width;
+    double p = 0.0;
+    int32_t c = 0;
+    if (e < E)
+        for (int64_t b = lo + part; b < hi; b += parts) {
+            p += ws.psum[b * E + e];
+            c += ws.csum[b * E + e];
+        }
+    sp[threadIdx.x] = p;
+    sc[threadIdx.x] = c;
+    __syncthreads();
+    double l = 0.0;
+    if (part == 0 && e < E) {
+        for (int i = 1; i < parts; ++i) {
+            p += sp[i * width + e];
+            c += sc[i * width + e];
+        }
+        const double nn = n;
+        const double f = n > 0 ? static_cast<double>(alpha) * E * c / (k * nn * nn * some) : 0.0;
+        counts[static_cast<int64_t>(s) * E + e] = c;
+        coef[static_cast<int64_t>(s) * E + e] = static_cast<float>(f);
+        l = n > 0 ? f * p : 0.0;
+    }
+    l = block_sum(l, red);
+    if (S == 1) {
+        if (threadIdx.x == 0) *loss = static_cast<float>(l);
+        return;
+    }
+    // the last block to come adds the sequences' losses (the ticket was cleared
+    // by the kernel before); nobody waits for anybody
+    if (threadIdx.x == 0) {
+        __hip_atomic_store(&ws.seq_loss[s], l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const int got = __hip_atomic_fetch_add(ws.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        last = got == S - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    l = 0.0;
+    for (int i = threadIdx.x; i < S; i += 1024)
+        l += __hip_atomic_load(&ws.seq_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    l = block_sum(l, red);
+    if (threadIdx.x == 0) *loss = static_cast<float>(l);
+}
+
+template <int LT, int QQ>
+__global__ __launch_bounds__(64 * kWaves) void balance_bwd_kernel(const float *__restrict__ logits, int64_t T, int E,
+                                                                  BalanceArgs b, float *__restrict__ dlogits) {
+    constexpr int TPW = 64 / LT;
+    const int lane = threadIdx.x & 63;
+    const int r = lane % LT;
+    const int64_t t = (static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6)) * TPW + lane / LT;
+    auto ex = [&](int q) { return 4 * (r + LT * (q >> 2)) + (q & 3); };
+    const int s = b.seq_offsets ? find_sequence<LT>(b.seq_offsets, b.S, t) : 0;
+    const bool live = t < T && s >= 0 && s < b.S && (!b.mask || b.mask[t] != 0);
+    float p[QQ], g[QQ];
+    token_softmax<LT, QQ>(logits + t * E, live, r, E, p);
+    const float *co = b.coef + static_cast<int64_t>(live ? s : 0) * E;
+    const float up = b.dloss ? *b.dloss : 1.0f;
+    float c = 0.0f;
+#pragma unroll
+    for (int q = 0; q < QQ; ++q) {
+        g[q] = live && ex(q) < E ? co[ex(q)] : 0.0f;
+        c = __builtin_fmaf(p[q], g[q], c);
+    }
+#pragma unroll
+    for (int o = LT / 2; o > 0; o >>= 1) c += __shfl_xor(c, o, 64);
+    if (t >= T) return;
+    // tokens that do not count get zeros, whatever their logits
+    float *row = dlogits + t * E;
+#pragma unroll
+    for (int q = 0; q < QQ; ++q) g[q] = live ? up * p[q] * (g[q] - c) : 0.0f;
+    if (E % 4 == 0) {
+#pragma unroll
+        for (int q = 0; q < QQ; q += 4)
+            if (ex(q) < E) *reinterpret_cast<float4 *>(row + ex(q)) = make_float4(g[q], g[q + 1], g[q + 2], g[q + 3]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < QQ; ++q)
+            if (ex(q) < E) row[ex(q)] = g[q];
+    }
+}
+
+// Lanes per token and experts per lane: at most 16 experts a lane up to 512
+#define XMOE_BALANCE_SHAPE(E, CALL)      \
+    do {                                 \
+        if ((E) <= 32) CALL(8, 4);       \
+        else if ((E) <= 64) CALL(16, 4); \
+        else if ((E) <= 128) CALL(16, 8); \
+        else if ((E) <= 192) CALL(16, 12); \
+        else if ((E) <= 256) CALL(16, 16); \
+        else if ((E) <= 512) CALL(32, 16); \
+        else CALL(32, 32);               \
+    } while (0)
+
+}  // namespace
+
+size_t balance_workspace(int64_t T, int E, int S) { return balance_ws(nullptr, T, E, S).bytes; }
+
+hipError_t launch_balance_loss(const float *logits, const int32_t *ids, int64_t T, int E, int k,
+                               const int32_t *seq_offsets, int S, const uint8_t *mask, float alpha, float *loss,
+                               int32_t *counts, float *coef, void *ws, hipStream_t st) {
+    const BalanceWs w = balance_ws(ws, T, E, S);
+    const int chunk = chunk_tokens(T);
+    // one block at least: it clears the ticket
+    const unsigned blocks = static_cast<unsigned>(std::max<int64_t>((T + chunk - 1) / chunk, 1));
+#define XMOE_BALANCE_PART(LT, QQ)                                                                                  \
+    hipLaunchKernelGGL((balance_part_kernel<LT, QQ>), dim3(blocks), dim3(64 * kWaves), 0, st, logits, ids, T, E, k, \
+                       seq_offsets, S, mask, chunk, w)
+    XMOE_BALANCE_SHAPE(E, XMOE_BALANCE_PART);
+#undef XMOE_BALANCE_PART
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(balance_final_kernel, dim3(static_cast<unsigned>(S)), dim3(1024), 0, st, T, E, k, seq_offsets,
+                       S, chunk, alpha, w, loss, counts, coef);
+    return hipGetLastError();
+}
+
+hipError_t launch_balance_loss_bwd(const float *logits, int64_t T, int E, const BalanceArgs &b, float *dlogits,
+                                   hipStream_t st) {
+    if (T <= 0) return hipSuccess;
+#define XMOE_BALANCE_BWD(LT, QQ)                                                                                     \
+    hipLaunchKernelGGL((balance_bwd_kernel<LT, QQ>),                                                                 \
+                       dim3(static_cast<unsigned>((T + kWaves * (64 / (LT)) - 1) / (kWaves * (64 / (LT))))),         \
+                       dim3(64 * kWaves), 0, st, logits, T, E, b, dlogits)
+    XMOE_BALANCE_SHAPE(E, XMOE_BALANCE_BWD);
+#undef XMOE_BALANCE_BWD
+    return hipGetLastError();
+}
+
+}  // namespace xmoe

@@ -97,4 +97,47 @@ hipError_t launch_ffn_bwd(int dt, const void *xs, const void *w1, const void *w3
                           int h, void *dh13, void *dxs, bool accumulate_dxs, void *dw1, void *dw3, void *dw2,
                           int grad_dt, bool accumulate_dw, hipStream_t s);
 
+// The tokens that the balance loss counts, by sequence, and what its gradient
+// needs: coef[s, e] = d loss / d p[t, e] for the tokens t of sequence s.
+struct BalanceArgs {
+    const int32_t *seq_offsets;  // [S + 1]; nullptr: one sequence, all tokens
+    int S;
+    const uint8_t *mask;         // [T]; nullptr: every token counts
+    const float *coef;           // [S, E]
+    const float *dloss;          // device scalar; nullptr: 1
+};
+size_t balance_workspace(int64_t T, int E, int S);
+hipError_t launch_balance_loss(const float *logits, const int32_t *ids, int64_t T, int E, int k,
+                               const int32_t *seq_offsets, int S, const uint8_t *mask, float alpha, float *loss,
+                               int32_t *counts, float *coef, void *ws, hipStream_t s);
+hipError_t launch_balance_loss_bwd(const float *logits, int64_t T, int E, const BalanceArgs &b, float *dlogits,
+                                   hipStream_t s);
+// launch_route_bwd with the balance loss's gradient added to the probabilities'
+hipError_t launch_route_bwd_balance(int dt, const void *x, const void *wg, const float *logits,
+                                    const int32_t *topk_ids, const float *dtopk_w, int ldw, int64_t T, int d, int E,
+                                    int k, float inv_tau, bool accumulate, const BalanceArgs &b, void *dx, float *dwg,
+                                    void *ws, hipStream_t s);
+
+// residual addition + root-mean-square norm (res, sum, y, q + scale, rstd may be nullptr)
+hipError_t launch_add_rmsnorm(int dt, const void *x, const void *res, const void *gamma, int64_t T, int d, float eps,
+                              void *sum, void *y, void *q, void *scale, float *rstd, hipStream_t s);
+size_t add_rmsnorm_bwd_workspace(int64_t T, int d, int dt);
+hipError_t launch_add_rmsnorm_bwd(int dt, const void *dy, const void *dsum, const void *sum, const void *gamma,
+                                  const float *rstd, int64_t T, int d, void *dx, float *dgamma, void *ws,
+                                  hipStream_t s);
+
+// 8-bit rows with block scales (mx8.hpp) and the expert FFN on them
+hipError_t launch_mx8_quantize(int dt, const void *x, int64_t n, int K, void *q, void *scale, hipStream_t s);
+hipError_t launch_mx8_dequantize(int dt, const void *q, const void *scale, int64_t n, int K, void *out,
+                                 hipStream_t s);
+// w [E, K, N] -> q [E, N, K], scale [E, ceil(K / 128), N, 4]
+hipError_t launch_mx8_quantize_weights(int dt, const void *w, int E, int K, int N, void *q, void *scale,
+                                       hipStream_t s);
+// row_map: nullptr (rows of xq) or token ids (rows of xq, which has map_rows rows)
+hipError_t launch_ffn_up_mx8(const void *xq, const void *xscale, const int32_t *row_map, int64_t map_rows,
+                             const void *w1, const void *w1s, const void *w3, const void *w3s, const int32_t *offsets,
+                             int E, int64_t rows, int d, int h, void *act, void *act_scale, hipStream_t s);
+hipError_t launch_ffn_down_mx8(const void *act, const void *act_scale, const void *w2, const void *w2s,
+                               const int32_t *offsets, int E, int64_t rows, int d, int h, void *ye, hipStream_t s);
+
 }  // namespace xmoe

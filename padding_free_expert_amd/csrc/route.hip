@@ -16,6 +16,7 @@
 // Wg's gradient, which a last kernel sums in a fixed order.
 #include <algorithm>
 
+#include "balance.hpp"
 #include "common.hpp"
 #include "gemm.hpp"
 #include "kernels.hpp"
@@ -310,11 +311,14 @@ __global__ __launch_bounds__(64 * NWV) void route_fused_kernel(const bf16_t *__r
 // the top-k kernel's layout: LT lanes per token, lane r holding the 16-byte
 // chunks r, r + LT, ... of the token's row.  The token's slots arrive LT at a
 // time, one per lane, and are broadcast within the token's lanes.
-template <int LT, int QQ, typename OutT>
+// BAL adds the balance loss's gradient of the probabilities, coef of the
+// token's sequence times the loss's upstream gradient, to g: no pass of its own.
+template <int LT, int QQ, typename OutT, bool BAL>
 __global__ __launch_bounds__(256) void route_dz_kernel(const float *__restrict__ logits,
                                                        const int32_t *__restrict__ ids,
                                                        const float *__restrict__ dw, int ldw, int64_t T, int E,
-                                                       int k, float inv_tau, OutT *__restrict__ dz) {
+                                                       int k, float inv_tau, OutT *__restrict__ dz,
+                                                       BalanceArgs bal) {
     static_assert(LT == 8 || LT == 16 || LT == 32, "lanes per token");
     static_assert(QQ % 4 == 0, "whole 16-byte chunks");
     constexpr int TPW = 64 / LT;
@@ -366,6 +370,16 @@ __global__ __launch_bounds__(256) void route_dz_kernel(const float *__restrict__
 #pragma unroll
             for (int q = 0; q < QQ; ++q)
                 if (ex(q) == ej) g[q] = gj;
+        }
+    }
+    if constexpr (BAL) {
+        const int sq = bal.seq_offsets ? find_sequence<LT>(bal.seq_offsets, bal.S, t) : 0;
+        if (live && sq >= 0 && sq < bal.S && (!bal.mask || bal.mask[t] != 0)) {
+            const float up = bal.dloss ? *bal.dloss : 1.0f;
+            const float *co = bal.coef + static_cast<int64_t>(sq) * E;
+#pragma unroll
+            for (int q = 0; q < QQ; ++q)
+                if (ex(q) < E) g[q] = __builtin_fmaf(up, co[ex(q)], g[q]);
         }
     }
     float c = 0.0f;
@@ -547,15 +561,15 @@ size_t route_bwd_workspace(int64_t T, int d, int E, int dt) {
     return dz + part;
 }
 
-template <typename OutT>
+template <typename OutT, bool BAL>
 static void launch_dz(int E, hipStream_t s, const float *logits, const int32_t *ids, const float *dw, int ldw,
-                      int64_t T, int k, float inv_tau, OutT *dz) {
+                      int64_t T, int k, float inv_tau, OutT *dz, const BalanceArgs &bal) {
     const int lt = lanes_per_token(T, E);
     const int qq = ((E + lt - 1) / lt + 3) / 4 * 4;
 #define XMOE_DZ(LT, QQ)                                                                                       \
-    hipLaunchKernelGGL((route_dz_kernel<LT, QQ, OutT>),                                                       \
+    hipLaunchKernelGGL((route_dz_kernel<LT, QQ, OutT, BAL>),                                                       \
                        dim3(static_cast<unsigned>((T + kWaves * (64 / LT) - 1) / (kWaves * (64 / LT)))),      \
-                       dim3(256), 0, s, logits, ids, dw, ldw, T, E, k, inv_tau, dz)
+                       dim3(256), 0, s, logits, ids, dw, ldw, T, E, k, inv_tau, dz, bal)
 #define XMOE_DZ_QQ(LT)                                                                                        \
     switch (qq) {                                                                                             \
         case 4: XMOE_DZ(LT, 4); break;                                                                        \
@@ -578,19 +592,26 @@ static void launch_dz(int E, hipStream_t s, const float *logits, const int32_t *
 #undef XMOE_DZ
 }
 
-hipError_t launch_route_bwd(int dt, const void *x, const void *wg, const float *logits, const int32_t *topk_ids,
+static hipError_t route_bwd(int dt, const void *x, const void *wg, const float *logits, const int32_t *topk_ids,
                             const float *dtopk_w, int ldw, int64_t T, int d, int E, int k, float inv_tau,
-                            bool accumulate, void *dx, float *dwg, void *ws, hipStream_t s) {
+                            bool accumulate, const BalanceArgs *bal, void *dx, float *dwg, void *ws, hipStream_t s) {
     const int S = rbwd_splits(T, d, E);
     const size_t dz_bytes = align256(static_cast<size_t>(T) * E * (dt == kBF16 ? 2 : 4));
     void *dz = ws;
     float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + dz_bytes);
     hipError_t err;
     if (T > 0) {
-        if (dt == kBF16)
-            launch_dz<bf16_t>(E, s, logits, topk_ids, dtopk_w, ldw, T, k, inv_tau, static_cast<bf16_t *>(dz));
+        const BalanceArgs none{};
+        auto *dzb = static_cast<bf16_t *>(dz);
+        auto *dzf = static_cast<float *>(dz);
+        if (dt == kBF16 && bal)
+            launch_dz<bf16_t, true>(E, s, logits, topk_ids, dtopk_w, ldw, T, k, inv_tau, dzb, *bal);
+        else if (dt == kBF16)
+            launch_dz<bf16_t, false>(E, s, logits, topk_ids, dtopk_w, ldw, T, k, inv_tau, dzb, none);
+        else if (bal)
+            launch_dz<float, true>(E, s, logits, topk_ids, dtopk_w, ldw, T, k, inv_tau, dzf, *bal);
         else
-            launch_dz<float>(E, s, logits, topk_ids, dtopk_w, ldw, T, k, inv_tau, static_cast<float *>(dz));
+            launch_dz<float, false>(E, s, logits, topk_ids, dtopk_w, ldw, T, k, inv_tau, dzf, none);
         if ((err = hipGetLastError()) != hipSuccess) return err;
 
         // dx[t] += dz[t] . Wg^T (or dx[t] = ... without accumulate) : A = dz [T,E]
@@ -652,6 +673,20 @@ hipError_t launch_route_bwd(int dt, const void *x, const void *wg, const float *
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 4096));
     hipLaunchKernelGGL(sum_partials_kernel, dim3(blocks), dim3(256), 0, s, part, S, n, dwg);
     return hipGetLastError();
+}
+
+hipError_t launch_route_bwd(int dt, const void *x, const void *wg, const float *logits, const int32_t *topk_ids,
+                            const float *dtopk_w, int ldw, int64_t T, int d, int E, int k, float inv_tau,
+                            bool accumulate, void *dx, float *dwg, void *ws, hipStream_t s) {
+    return route_bwd(dt, x, wg, logits, topk_ids, dtopk_w, ldw, T, d, E, k, inv_tau, accumulate, nullptr, dx, dwg, ws,
+                     s);
+}
+
+hipError_t launch_route_bwd_balance(int dt, const void *x, const void *wg, const float *logits,
+                                    const int32_t *topk_ids, const float *dtopk_w, int ldw, int64_t T, int d, int E,
+                                    int k, float inv_tau, bool accumulate, const BalanceArgs &b, void *dx, float *dwg,
+                                    void *ws, hipStream_t s) {
+    return route_bwd(dt, x, wg, logits, topk_ids, dtopk_w, ldw, T, d, E, k, inv_tau, accumulate, &b, dx, dwg, ws, s);
 }
 
 }  // namespace xmoe

@@ -1,0 +1,244 @@
+"""8-bit rows with block scales, and the experts' FFN on them, against the
+64-bit definition.
+
+Bounds.  Quantizing given values is exact arithmetic and one rounding: the
+bytes must be equal.  The matrix instruction adds eight products at a time,
+each cut at 2^-13 of the power of two of the largest (on the card: 2^16 + x -
+2^16 within eight neighbours keeps x = 2^3 and loses 2^2; in different eights
+it keeps 2^-7), and the eights' sums in fp32: seven cut terms of an eight lose
+less than 7 * 2^-13 of its largest, so all together less than 2^-10 of the sum
+of the magnitudes, and K additions K 2^-24 of it.  silu multiplies that by its slope, at most 1.1,
+and adds a few roundings (2^-19 relative); act's 8 bits add 2^-4 of an element
+or half of the smallest step (2^-10 times the scale); ye adds bf16's half step."""
+import pytest
+import torch
+
+import _block_ref as br
+from _helpers import need_gpu
+
+pytestmark = pytest.mark.gpu
+F8, U8, BF = torch.float8_e4m3fn, torch.uint8, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def xm():
+    need_gpu()
+    import padding_free_expert_amd as m
+    assert m.xmoe_query_device(0)
+    return m
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _quantize(xm, x, G=None):
+    n, K = x.shape
+    new = G.empty if G else (lambda s, dt: torch.empty(s, dtype=dt, device="cuda"))
+    q, s = new((n, K), F8), new(xm.mx8_scale_shape(n, K), U8)
+    xm.xmoe_mx8_quantize(x, q, s)
+    return q, s
+
+
+def _same_bytes(q, s, x):
+    """q, s against float64 rows x."""
+    b = br.mx8_bytes(x)
+    got, pad = br.scale_bytes(s, x.shape[1])
+    assert torch.equal(got, b), "scale bytes"
+    assert bool((pad == 127).all()), "padding bytes"
+    want, have = br.mx8_round(x, b), br.mx8_values(q, s)
+    nan = torch.isnan(want)
+    assert torch.equal(nan, torch.isnan(have)) and torch.equal(want[~nan], have[~nan]), "elements"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,K", [(1, 32), (1, 2048), (3, 96), (5, 160), (7, 7168), (130, 512), (1000, 1408), (65, 544), (2, 65536)])
+def test_rows_there_and_back(xm, n, K, dtype):
+    print(f"[mx8] n={n} K={K} {dtype}", flush=True)
+    dt = BF if dtype == "bf16" else torch.float32
+    g = _gen(n + K)
+    x = (torch.randn((n, K), generator=g, device="cuda") * torch.exp(4 * torch.randn((n, K // 32, 1), generator=g, device="cuda")).expand(n, K // 32, 32).reshape(n, K)).to(dt)
+    G = br.Guarded()
+    q, s = _quantize(xm, x, G)
+    _same_bytes(q, s, x.double())
+    for od in (BF, torch.float32):
+        out = G.empty((n, K), od)
+        xm.xmoe_mx8_dequantize(q, s, out)
+        assert torch.equal(out.double(), br.mx8_values(q, s))
+    G.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_borders_of_the_format(xm, dtype):
+    """Maxima next to 448 * 2^e, ties between two elements, subnormal elements,
+    zeros, the largest and smallest magnitudes, infinities and NaNs."""
+    dt = BF if dtype == "bf16" else torch.float32
+    rows = []
+    for e in (-140, -133, -120, -20, -1, 0, 3, 60, 118, 119):
+        for top in (448.0, 450.0, 446.0, 256.0, 255.0):
+            b = torch.zeros(32, dtype=torch.float64)
+            b[0] = top
+            b[1:16] = torch.tensor([1.0625 * 2, 1.1875 * 2, -1.0625 * 16, 17.0, 18.0, 2.0 ** -9, 2.0 ** -10, 3 * 2.0 ** -10,
+                                    -2.0 ** -6, 1.5 * 2.0 ** -6, 240.0, 232.0, 248.0, 104.0, 108.0])
+            rows.append(torch.ldexp(b, torch.tensor(e)))
+    x = torch.stack(rows).to(dt).cuda()
+    x = torch.cat([x, torch.zeros_like(x[:1]), -torch.zeros_like(x[:1]), x[5:8]])
+    x[-1, 3], x[-2, 4], x[-3, 5] = float("nan"), float("inf"), float("-inf")
+    x = torch.cat([x, x.flip(0)], 1)
+    q, s = _quantize(xm, x)
+    _same_bytes(q, s, x.double())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("E,K,N", [(1, 32, 32), (2, 96, 64), (3, 160, 96), (4, 256, 1056), (2, 1408, 160)])
+def test_weights(xm, E, K, N, dtype):
+    dt = BF if dtype == "bf16" else torch.float32
+    w = torch.randn((E, K, N), generator=_gen(E + K), device="cuda").to(dt)
+    w[0, 5, 7] = float("inf")
+    w[E - 1, :32, 3] = 0
+    G = br.Guarded()
+    q, s = G.empty((E, N, K), F8), G.empty((E,) + xm.mx8_scale_shape(N, K), U8)
+    xm.xmoe_mx8_quantize_weights(w, q, s)
+    G.check()
+    for e in range(E):
+        _same_bytes(q[e], s[e], w[e].t().double())
+
+
+def _experts(xm, E, d, h, seed):
+    g = _gen(seed)
+    out = []
+    for N, K in ((h, d), (h, d), (d, h)):
+        w = (torch.randn((E, K, N), generator=g, device="cuda") * K ** -0.5).to(BF)
+        q = torch.empty((E, N, K), dtype=F8, device="cuda")
+        s = torch.empty((E,) + xm.mx8_scale_shape(N, K), dtype=U8, device="cuda")
+        xm.xmoe_mx8_quantize_weights(w, q, s)
+        out += [q, s]
+    return out
+
+
+def _rows(counts):
+    off = torch.zeros(len(counts) + 1, dtype=torch.int32)
+    off[1:] = torch.cumsum(torch.tensor(counts), 0).to(torch.int32)
+    return off.cuda(), int(sum(counts))
+
+
+def _check_experts(xm, counts, d, h, T=None, seed=0, spare=0, tweak=None):
+    """One pair of products on experts of the given row counts; `spare` rows
+    behind the last segment; T: rows of x gathered by token id."""
+    E = len(counts)
+    w1, w1s, w3, w3s, w2, w2s = _experts(xm, E, d, h, seed)
+    off, used = _rows(counts)
+    rows = used + spare
+    g = _gen(seed + 1)
+    n = rows if T is None else T
+    x = torch.randn((n, d), generator=g, device="cuda").to(BF)
+    if tweak:
+        tweak(x)
+    ids = None if T is None else torch.randint(0, T, (rows,), generator=g, device="cuda").to(torch.int32)
+    xq, xs = _quantize(xm, x)
+    G = br.Guarded()
+    act, acts, ye = G.empty((rows, h), F8), G.empty(xm.mx8_scale_shape(rows, h), U8), G.empty((rows, d), BF)
+    act.view(U8).fill_(0x11)
+    acts.fill_(0x77)
+    ye.view(torch.int16).fill_(0x1234)
+    xm.xmoe_expert_ffn_up_mx8(xq, xs, w1, w1s, w3, w3s, off, act, acts, token_ids=ids)
+    xm.xmoe_expert_ffn_down_mx8(act, acts, w2, w2s, off, ye)
+    G.check()
+    # rows behind the last segment stay as they were
+    assert bool((act.view(U8)[used:] == 0x11).all()) and bool((acts[:, used:] == 0x77).all())
+    assert bool((ye.view(torch.int16)[used:] == 0x1234).all())
+    xv = br.mx8_values(xq, xs)
+    if ids is not None:
+        xv = xv[ids.long()]
+    av = br.mx8_values(act[:used], acts[:, :used].contiguous())
+    pad = br.scale_bytes(acts[:, :used].contiguous(), h)[1]
+    assert bool((pad == 127).all()), "padding bytes of act's scales"
+    lo = 0
+    for e, c in enumerate(counts):
+        if c:
+            sl = slice(lo, lo + c)
+            a1, a3 = (br.mx8_values(w[e], s[e]) for w, s in ((w1, w1s), (w3, w3s)))
+            H1, H3 = xv[sl] @ a1.t(), xv[sl] @ a3.t()
+            e1, e3 = ((2.0 ** -10 + d * 2.0 ** -24) * (xv[sl].abs() @ a.abs().t()) for a in (a1, a3))
+            ref = H1 * torch.sigmoid(H1) * H3
+            tol = 1.1 * e1 * (H3.abs() + e3) + (H1 * torch.sigmoid(H1)).abs() * e3 + 2.0 ** -19 * ref.abs()
+            sc = torch.exp2(br.scale_bytes(acts[:, sl].contiguous(), h)[0].double() - 127).repeat_interleave(32, 1)
+            br.close(av[sl], ref, 2.0 ** -4, 1.07 * tol + 2.0 ** -10 * sc, f"act of expert {e}")
+            # the scale is the least that the block's magnitudes allow
+            big = (ref.abs() + tol).reshape(c, -1, 32).amax(-1)
+            small = (ref.abs() - tol).clamp(min=0).reshape(c, -1, 32).amax(-1)
+            s32 = sc[:, ::32]
+            fine = ~torch.isnan(big)
+            assert bool(((small <= 448 * s32) & (big > 224 * s32))[fine].all()), "act's scales"
+            a2 = br.mx8_values(w2[e], w2s[e])
+            yr = av[sl] @ a2.t()
+            br.close(ye[sl], yr, br.half_step(BF), 1.01 * (2.0 ** -10 + h * 2.0 ** -24) * (av[sl].abs() @ a2.abs().t()),
+                     f"ye of expert {e}")
+            # those worst cases do not come together: over many values bf16's rounding
+            # (rms: half a step over the root of 3) leaves them room below half a step
+            if c * d >= 4096 and not torch.isnan(yr).any():
+                assert float((ye[sl].double() - yr).norm() / yr.norm()) <= br.half_step(BF)
+        lo += c
+    return act, acts, ye
+
+
+@pytest.mark.parametrize("counts,d,h,T", [
+    ([1], 32, 32, None), ([1], 128, 32, 1), ([0, 3, 0], 96, 64, 5), ([17, 0, 16, 15], 160, 96, 20),
+    ([33, 1, 31, 32, 64], 288, 160, None), ([5, 0, 0, 200, 7], 256, 224, 100), ([300], 128, 1056, 64),
+    ([129, 127, 128], 544, 128, 50), ([2, 1, 0, 1, 0, 0, 2, 1], 2048, 1408, 1), ([257, 511, 256, 0, 3], 384, 416, 700),
+    ([1030, 70], 64, 640, 300), ([600, 900], 1024, 256, None)])
+def test_experts(xm, counts, d, h, T):
+    print(f"[experts8] counts={counts} d={d} h={h} T={T}", flush=True)
+    _check_experts(xm, counts, d, h, T, seed=len(counts) + d)
+
+
+def test_experts_with_rows_behind_the_last_segment(xm):
+    _check_experts(xm, [40, 0, 9], 192, 96, 30, spare=21)
+    _check_experts(xm, [400, 0, 300], 192, 160, None, spare=130)
+
+
+@pytest.mark.parametrize("counts", [[3, 20], [300, 260]])
+def test_a_nan_stays_in_its_row(xm, counts):
+    def tweak(x):
+        x[2, 40] = float("nan")
+        x[5, 0] = float("inf")
+    act, acts, ye = _check_experts(xm, counts, 128, 96, None, tweak=tweak)
+    bad = torch.isnan(ye.float()).any(1)
+    assert torch.nonzero(bad).flatten().tolist() == [2, 5]
+
+
+def test_ids_outside_the_rows_read_zeros(xm):
+    for c in (5, 300):
+        d, h = 64, 64
+        w1, w1s, w3, w3s, w2, w2s = _experts(xm, 1, d, h, 3)
+        xq, xs = _quantize(xm, torch.randn((c, d), generator=_gen(1), device="cuda").to(BF))
+        ids = torch.arange(c, dtype=torch.int32, device="cuda")
+        off = torch.tensor([0, c], dtype=torch.int32, device="cuda")
+        act, acts = torch.empty((c, h), dtype=F8, device="cuda"), torch.empty(xm.mx8_scale_shape(c, h), dtype=U8, device="cuda")
+        xm.xmoe_expert_ffn_up_mx8(xq, xs, w1, w1s, w3, w3s, off, act, acts, token_ids=ids)
+        want = br.mx8_values(act, acts)
+        ids[1], ids[3], ids[4] = -1, c, 1 << 30
+        xm.xmoe_expert_ffn_up_mx8(xq, xs, w1, w1s, w3, w3s, off, act, acts, token_ids=ids)
+        want[1] = want[3] = want[4] = 0
+        assert torch.equal(br.mx8_values(act, acts), want)
+
+
+def test_no_rows(xm):
+    w1, w1s, w3, w3s, w2, w2s = _experts(xm, 2, 64, 32, 0)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    x = torch.empty((0, 64), dtype=BF, device="cuda")
+    xq, xs = _quantize(xm, x)
+    act, acts = torch.empty((0, 32), dtype=F8, device="cuda"), torch.empty((1, 0, 4), dtype=U8, device="cuda")
+    xm.xmoe_expert_ffn_up_mx8(xq, xs, w1, w1s, w3, w3s, off, act, acts)
+    xm.xmoe_expert_ffn_down_mx8(act, acts, w2, w2s, off, torch.empty((0, 64), dtype=BF, device="cuda"))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("counts", [[3, 0, 12], [700, 90, 300]])
+def test_the_same_bits_again(xm, counts):
+    a = _check_experts(xm, counts, 512, 192, 64)
+    b = _check_experts(xm, counts, 512, 192, 64)
+    for x, y in zip(a, b):
+        assert torch.equal(x.view(U8), y.view(U8))
