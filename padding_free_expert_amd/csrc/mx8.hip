@@ -23,6 +23,7 @@ namespace xmoe {
 
 namespace {
 
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
@@ -299,6 +300,248 @@ __global__ __launch_bounds__(64 * KW) void mx8_stream_kernel(Mx8Args p) {
     }
 }
 
+// Many rows per expert: 256 x 256 results a block (NB = 2: 128 columns of W1 and
+// the same of W3), four waves of 128 x 128, one block per compute unit.  Both
+// operands come into an S-slot ring of shared memory by direct loads, 64 bytes
+// of K a slot, in the layout and with the swizzle of the bf16 products (a
+// 16-byte chunk here is 16 elements instead of 8); the scale dwords of 128 of K
+// (two slots) come the same way.  Wave tiles this wide are what the rates ask
+// for: per 64 of K a wave reads 16 KiB from shared memory for 16 products of 64
+// cycles; 64 x 128 tiles would read 12 KiB for 8, and with the ring's own
+// writes shared memory would be busy longer than the matrix cores.
+//
+// Step `it` multiplies slot it's fragments, already in registers, while those
+// of slot it + 1 are read.  It starts with the one wait and barrier of the step:
+// slot it + 1 has landed, and every wave has read slot it, which then takes the
+// loads of it + S.
+template <int NB, int S>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx8_tile_kernel(Mx8Args p) {
+    constexpr int BM = 256, BN = 256 / NB, WGM = 2, WGN = 2, NW = 4;
+    constexpr int WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32, TT = NB * TN;
+    static_assert(TM == 4 && TT == 4, "sixteen 32 x 32 results a wave");
+    using PA = DmaPlan<BM, 32, true, NW>;  // in 2-byte units: 64 bytes of K
+    using PB = DmaPlan<BN, 32, true, NW>;
+    constexpr int kABytes = PA::kBytes, kBBytes = PB::kBytes, kStage = kABytes + NB * kBBytes;
+    constexpr int kL = PA::kN + NB * PB::kN;         // operand loads of a wave per slot
+    constexpr int kScales = 512 * 4, kScaleSlots = 4;  // scale dwords of 256 + 256 rows
+    constexpr int kRing = S * kStage;
+    static_assert(S == 4, "the waits count two slots behind the next, one of each parity");
+    static_assert(kRing + kScaleSlots * kScales <= 160 * 1024 - 64, "one block per compute unit");
+    __shared__ __align__(1024) char smem[kRing + kScaleSlots * kScales];
+
+    Tile t;
+    if (!resolve_tile<BM, BN>(p.g, &t, blockIdx.x, gridDim.x)) return;
+    const int N = p.g.N, K = p.K, kb = (K + 127) / 128;
+    const int m0 = t.m0, n0 = t.nt * BN;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WGN, wn = wave % WGN, half = lane >> 5;
+    const uint32_t sbase = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+    const bool wact = m0 + wm * WTM < t.Mg && n0 + wn * WTN < N;
+    const int total = (K + 63) / 64;
+
+    // operand loads: rows past the group's or N, and K's end, load zeros
+    PA pa;
+    PB pb;
+    __amdgpu_buffer_rsrc_t ra, rb[NB];
+    const int32_t *map = p.map ? p.map + t.base + m0 : nullptr;
+    if (map) {
+        pa.init_mapped(wave, lane, K / 2, map, t.Mg - m0, K / 2);
+#pragma unroll
+        for (int i = 0; i < PA::kN; ++i) {  // ids outside the rows: zeros
+            const int row = ((i * NW + wave) * 1024 + lane * 16) / PA::kRowBytes;
+            const int id = row < t.Mg - m0 ? map[row] : 0;
+            if (id < 0 || id >= p.a_rows) pa.lim[i] = INT_MIN;
+        }
+        ra = make_rsrc(p.a, p.a_rows * K);
+    } else {
+        pa.init(wave, lane, K / 2, 0, t.Mg - m0, K / 2);
+        ra = make_rsrc(p.a + (t.base + m0) * K, static_cast<int64_t>(t.Mg - m0) * K);
+    }
+    pb.init(wave, lane, K / 2, 0, N - n0, K / 2);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+        rb[b] = make_rsrc((b ? p.b1 : p.b0) + (static_cast<int64_t>(t.g) * N + n0) * K, static_cast<int64_t>(N - n0) * K);
+    // scale loads: wave w takes rows 64 w .. 64 w + 63 of A's 256 and of B's (of W1 and W3: 128 each)
+    int as_off = kOob, bs_off = kOob;
+    {
+        const int row = 64 * wave + lane;
+        if (row < t.Mg - m0) {
+            const int64_t id = map ? map[row] : t.base + m0 + row;
+            if (id >= 0 && id < p.a_rows) as_off = static_cast<int>(map ? id * 4 : row * 4);
+        }
+        const int col = NB == 2 ? row & 127 : row;
+        if (n0 + col < N) bs_off = col * 4;
+    }
+    const int64_t as_first = map ? 0 : t.base + m0;
+    const uint8_t *bsrc = (NB == 2 && wave >= 2) ? p.b1s : p.b0s;
+
+    auto issue_part = [&](int st, int part) {  // operand load `part` of slot st
+        const bool live = st < total;
+        const int kc = live ? st * 32 : INT_MAX, kadd = st * 64;
+        const uint32_t dst = sbase + (st & (S - 1)) * kStage;
+        if (part < PA::kN) {
+            pa.issue(ra, kc, kadd, dst, wave, part);
+        } else {
+            const int b = (part - PA::kN) / PB::kN, i = (part - PA::kN) % PB::kN;
+            pb.issue(rb[b], kc, kadd, dst + kABytes + b * kBBytes, wave, i);
+        }
+    };
+    auto issue_scales = [&](int st) {  // even slots: the scales of their 128 of K
+        const bool live = st < total;
+        const int64_t g = live ? st >> 1 : 0;
+        const uint32_t dst = sbase + kRing + ((st >> 1) & (kScaleSlots - 1)) * kScales + wave * 256;
+        const __amdgpu_buffer_rsrc_t rsa = make_rsrc(p.as + (g * p.a_rows + as_first) * 4, (p.a_rows - as_first) * 4);
+        const __amdgpu_buffer_rsrc_t rsb = make_rsrc(bsrc + ((static_cast<int64_t>(t.g) * kb + g) * N + n0) * 4,
+                                                     static_cast<int64_t>(N - n0) * 4);
+        lds_dma4(rsa, live ? as_off : kOob, dst);
+        lds_dma4(rsb, live ? bs_off : kOob, dst + 1024);
+    };
+
+    f32x16_t acc[NB][TM][TN];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[b][i][j][r] = 0.0f;
+
+    // fragment addresses: lane l reads chunks l / 32 and 2 + l / 32 of row l % 32
+    // (the swizzle goes by the row modulo 32, so whole 32-row blocks are immediates)
+    const int row = lane & 31, sw = swz_kc(row, 4);
+    const uint32_t flo = row * 64 + 16 * (half ^ sw), fhi = row * 64 + 16 * ((2 + half) ^ sw);
+    i32x8_t fA[2][TM], fB[2][TT];
+    int sA[2][TM], sB[2][TT];
+    typedef __attribute__((address_space(3))) const i32x4_t lds_i32x4;
+    auto frag = [&](uint32_t tile) {
+        const i32x4_t lo = *reinterpret_cast<lds_i32x4 *>(static_cast<uintptr_t>(tile + flo));
+        const i32x4_t hi = *reinterpret_cast<lds_i32x4 *>(static_cast<uintptr_t>(tile + fhi));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    auto read_unit = [&](int set, int st, int u) {
+        const uint32_t sa = sbase + (st & (S - 1)) * kStage;
+        if (u < TM) {
+            fA[set][u] = frag(sa + (wm * WTM + 32 * u) * 64);
+        } else {
+            const int b = (u - TM) / TN, j = (u - TM) % TN;
+            fB[set][u - TM] = frag(sa + kABytes + b * kBBytes + (wn * WTN + 32 * j) * 64);
+        }
+    };
+    auto read_scales = [&](int set, int st) {  // the scales of slot st's 128 of K
+        const uint32_t ss = sbase + kRing + ((st >> 1) & (kScaleSlots - 1)) * kScales;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sA[set][i] = lds_read_i32(ss + (wm * WTM + 32 * i + row) * 4) >> (8 * half);
+#pragma unroll
+        for (int u = 0; u < TT; ++u)
+            sB[set][u] = lds_read_i32(ss + 1024 + ((u / TN) * BN + wn * WTN + 32 * (u % TN) + row) * 4) >> (8 * half);
+    };
+
+#pragma unroll
+    for (int st = 0; st < S; ++st) {
+        if (st % 2 == 0) issue_scales(st);
+#pragma unroll
+        for (int u = 0; u < kL; ++u) issue_part(st, u);
+    }
+    wait_vmem<3 * kL + 2>();  // slot 0 has landed (slot 2 brings scales too)
+    __syncthreads();
+    auto k_loop = [&](auto active) {
+        constexpr bool ACT = decltype(active)::value;
+        if constexpr (ACT) {
+            read_scales(0, 0);
+#pragma unroll
+            for (int u = 0; u < TM + TT; ++u) read_unit(0, 0, u);
+        }
+        // P: parity of the slot; Q: of its 128 of K (register sets)
+        auto step = [&](int it, auto par, auto grp) {
+            constexpr int P = decltype(par)::value, Q = decltype(grp)::value;
+            wait_vmem<2 * kL + 2>();  // slots it + 2 and it + 3 may be in flight
+            __syncthreads();
+            if constexpr (P == 0) issue_scales(it + S);
+            if constexpr (ACT && P == 1) read_scales(Q ^ 1, it + 1);
+#pragma unroll
+            for (int q = 0; q < TM * TT; ++q) {
+                const int u = q / TM, i = q % TM;
+                if constexpr (ACT) {
+                    if (q < TM + TT) read_unit(P ^ 1, it + 1, q);
+                    acc[u / TN][i][u % TN] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        fB[P][u], fA[P][i], acc[u / TN][i][u % TN], 0, 0, 2 * P, sB[Q][u], 2 * P, sA[Q][i]);
+                }
+                if (q % 2 == 0 && q / 2 < kL) issue_part(it + S, q / 2);
+            }
+        };
+        constexpr std::integral_constant<int, 0> c0{};
+        constexpr std::integral_constant<int, 1> c1{};
+        for (int it = 0; it < total; it += 4) {
+            step(it, c0, c0);
+            if (it + 1 < total) step(it + 1, c1, c0);
+            if (it + 2 < total) step(it + 2, c0, c1);
+            if (it + 3 < total) step(it + 3, c1, c1);
+        }
+    };
+    if (wact) k_loop(std::true_type{});
+    else k_loop(std::false_type{});
+    wait_vmem<0>();  // no load may still target the ring
+    if constexpr (NB == 1) {
+        GroupPtrs<bf16_t> q{};
+        q.crow = t.base;
+        gemm_epilogue<BM, BN, WGM, WGN, 1, kRing, EPI_STORE, bf16_t>(p.g, t, q, acc, smem, sbase, m0, n0, lane, wave);
+    } else {
+        // lane l: row 32 i + l % 32, columns 32 j + 8 g + 4 (l / 32) + r; a block of
+        // 32 columns lies in lanes l and l ^ 32.  The bytes leave through the ring
+        // (rows of 144 bytes), 16 at a time, a row's four scale bytes as one dword.
+        constexpr int LDC = BN + 16;
+        char *const sc = smem + BM * LDC;
+        static_assert(BM * LDC + BM * 4 <= kRing, "staging");
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                float o[16];
+                uint32_t a = 0u;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float h1 = acc[0][i][j][r];
+                    o[r] = h1 * __builtin_amdgcn_rcpf(1.0f + __expf(-h1)) * acc[1][i][j][r];
+                    a = max(a, __float_as_uint(o[r]) & 0x7fffffffu);
+                }
+                a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), 32, 64)));
+                const uint32_t byte = mx8_scale_byte(a);
+                const float s = mx8_inv_scale(byte);
+                const int m = wm * WTM + 32 * i + row, c = wn * WTN + 32 * j;
+#pragma unroll
+                for (int r = 0; r < 16; r += 4)
+                    *reinterpret_cast<uint32_t *>(smem + m * LDC + c + 2 * r + 4 * half) =
+                        byte == 255u ? 0x7f7f7f7fu : mx8_pack4(o[r] * s, o[r + 1] * s, o[r + 2] * s, o[r + 3] * s);
+                // past N: the byte that fills the last group (a NaN row is NaN there too)
+                if (half == 0) sc[m * 4 + c / 32] = static_cast<char>(n0 + c < N ? byte : kMxOne);
+            }
+        __syncthreads();
+        const int rows = min(BM, t.Mg - m0);
+        for (int c = threadIdx.x; c < rows * (BN / 16); c += 256) {
+            const int m = c / (BN / 16), n = 16 * (c % (BN / 16));
+            if (n0 + n < N)
+                *reinterpret_cast<uint4 *>(p.q + (t.base + m0 + m) * N + n0 + n) =
+                    *reinterpret_cast<const uint4 *>(smem + m * LDC + n);
+        }
+        if (static_cast<int>(threadIdx.x) < rows)
+            *reinterpret_cast<uint32_t *>(p.qs + (static_cast<int64_t>(n0 / 128) * p.g.extent + t.base + m0 + threadIdx.x) * 4) =
+                *reinterpret_cast<const uint32_t *>(sc + 4 * threadIdx.x);
+    }
+}
+
+template <int NB>
+hipError_t launch_tile(const Mx8Args &p, hipStream_t s) {
+    constexpr int BM = 256, BN = 256 / NB;
+    const int64_t tiles = p.g.extent / BM + std::min<int64_t>(p.g.G, p.g.extent);
+    const int64_t grid = tiles * ((p.g.N + BN - 1) / BN);
+    if (grid <= 0) return hipSuccess;
+    hipLaunchKernelGGL((mx8_tile_kernel<NB, 4>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
 template <int NB, int MT, int KW>
 hipError_t launch_stream(const Mx8Args &p, hipStream_t s) {
     // no expert without rows has a tile: at most rows / BM whole ones and one
@@ -325,7 +568,9 @@ Mx8Args rows_args(const int32_t *offsets, int E, int64_t rows, int N, int K) {
 
 template <int NB>
 hipError_t product(const Mx8Args &p, hipStream_t s) {
-    return launch_stream<NB, 2, 8>(p, s);
+    // few rows per expert: the weights' bytes bound it
+    if (p.g.extent <= 48 * static_cast<int64_t>(p.g.G)) return launch_stream<NB, 2, 8>(p, s);
+    return launch_tile<NB>(p, s);
 }
 
 }  // namespace
@@ -393,6 +638,8 @@ hipError_t launch_ffn_down_mx8(const void *act, const void *act_scale, const voi
     p.b0 = static_cast<const uint8_t *>(w2);
     p.b0s = static_cast<const uint8_t *>(w2s);
     p.y = static_cast<bf16_t *>(ye);
+    p.g.C0 = ye;
+    p.g.ldc = d;
     return product<1>(p, s);
 }
 
