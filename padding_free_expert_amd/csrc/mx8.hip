@@ -127,7 +127,7 @@ __global__ __launch_bounds__(256) void mx8_quantize_weights_kernel(const T *__re
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float *p = &s[32 * g + 4 * i][threadIdx.x & 63];
-        o[i] = byte == 255u ? 0x7f7f7f7fu : mx8_pack4(p[0] * m, p[65] * m, p[130] * m, p[195] * m);
+        o[i] = mx8_pack4(p[0] * m, p[65] * m, p[130] * m, p[195] * m);
     }
     uint4 *dst = reinterpret_cast<uint4 *>(q + (static_cast<int64_t>(e) * N + n) * K + k0 + 32 * g);
     dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
@@ -135,6 +135,17 @@ __global__ __launch_bounds__(256) void mx8_quantize_weights_kernel(const T *__re
 }
 
 // ------------------------------------------------------------------ products
+
+// one block of the tile kernel for each (a multiple of the XCDs' number)
+constexpr int kComputeUnits = 256;
+
+// two fp32 -> packed bf16, round to nearest even
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    const f2 v = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf2));
+}
 
 struct Mx8Args {
     GemmArgs g;                 // what resolve_tile reads: GM_ROWS, offsets, G, extent, N
@@ -283,8 +294,7 @@ __global__ __launch_bounds__(64 * KW) void mx8_stream_kernel(Mx8Args p) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 *reinterpret_cast<uint32_t *>(p.q + row * N + n0 + 16 * j + 4 * quad) =
-                    byte == 255u ? 0x7f7f7f7fu
-                                 : mx8_pack4(o[4 * j] * sc, o[4 * j + 1] * sc, o[4 * j + 2] * sc, o[4 * j + 3] * sc);
+                    mx8_pack4(o[4 * j] * sc, o[4 * j + 1] * sc, o[4 * j + 2] * sc, o[4 * j + 3] * sc);
             // the scale byte of this block of 32 columns; the last block also fills its group
             const int blk = n0 / 32;
             const int at = (blk & 3) + quad;
@@ -300,245 +310,424 @@ __global__ __launch_bounds__(64 * KW) void mx8_stream_kernel(Mx8Args p) {
     }
 }
 
-// Many rows per expert: 256 x 256 results a block (NB = 2: 128 columns of W1 and
-// the same of W3), four waves of 128 x 128, one block per compute unit.  Both
-// operands come into an S-slot ring of shared memory by direct loads, 64 bytes
-// of K a slot, in the layout and with the swizzle of the bf16 products (a
-// 16-byte chunk here is 16 elements instead of 8); the scale dwords of 128 of K
-// (two slots) come the same way.  Wave tiles this wide are what the rates ask
-// for: per 64 of K a wave reads 16 KiB from shared memory for 16 products of 64
-// cycles; 64 x 128 tiles would read 12 KiB for 8, and with the ring's own
-// writes shared memory would be busy longer than the matrix cores.
-//
-// Step `it` multiplies slot it's fragments, already in registers, while those
-// of slot it + 1 are read.  It starts with the one wait and barrier of the step:
-// slot it + 1 has landed, and every wave has read slot it, which then takes the
-// loads of it + S.
-template <int NB, int S>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx8_tile_kernel(Mx8Args p) {
-    constexpr int BM = 256, BN = 256 / NB, WGM = 2, WGN = 2, NW = 4;
-    constexpr int WTM = BM / WGM, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32, TT = NB * TN;
-    static_assert(TM == 4 && TT == 4, "sixteen 32 x 32 results a wave");
-    using PA = DmaPlan<BM, 32, true, NW>;  // in 2-byte units: 64 bytes of K
-    using PB = DmaPlan<BN, 32, true, NW>;
-    constexpr int kABytes = PA::kBytes, kBBytes = PB::kBytes, kStage = kABytes + NB * kBBytes;
-    constexpr int kL = PA::kN + NB * PB::kN;         // operand loads of a wave per slot
-    constexpr int kScales = 512 * 4, kScaleSlots = 4;  // scale dwords of 256 + 256 rows
-    constexpr int kRing = S * kStage;
-    static_assert(S == 4, "the waits count two slots behind the next, one of each parity");
-    static_assert(kRing + kScaleSlots * kScales <= 160 * 1024 - 64, "one block per compute unit");
-    __shared__ __align__(1024) char smem[kRing + kScaleSlots * kScales];
+// The tiles of a launch, found from the device-side offsets once per block and
+// kept in shared memory: for each expert its rows and the number of row tiles
+// up to and including its own.
+// A value that the compiler takes as new at this point: what follows from it is
+// computed here instead of being kept in registers across the loop around it.
+__device__ __forceinline__ uint32_t fresh(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
 
+// direct-to-LDS loads as those of gemm.hpp, with a scalar offset
+__device__ __forceinline__ void lds_dma16(__amdgpu_buffer_rsrc_t rs, uint32_t voff, uint32_t soff, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
+                 :
+                 : "v"(voff), "s"(rs), "s"(lds), "s"(soff)
+                 : "memory");
+}
+__device__ __forceinline__ void lds_dma4(__amdgpu_buffer_rsrc_t rs, uint32_t voff, uint32_t soff, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %3 offen lds"
+                 :
+                 : "v"(voff), "s"(rs), "s"(lds), "s"(soff)
+                 : "memory");
+}
+
+struct TileTable {
+    int end[1024];  // INT_MAX past the last expert
+    int lo[1024], hi[1024];
+    int wave_sum[4];
+};
+
+// Fills the table (256 threads; ends with a barrier).  Returns the row tiles.
+template <int BM>
+__device__ __forceinline__ int build_table(const GemmArgs &p, TileTable &tt) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int cnt[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int g = 4 * threadIdx.x + i;
+        int64_t lo = 0, hi = 0;
+        if (g < p.G) seg_bounds(p, g, &lo, &hi);
+        tt.lo[g] = static_cast<int>(lo);
+        tt.hi[g] = static_cast<int>(hi);
+        sum += static_cast<int>((hi - lo + BM - 1) / BM);
+        cnt[i] = sum;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int v = __shfl_up(inc, off, 64);
+        if (lane >= off) inc += v;
+    }
+    if (lane == 63) tt.wave_sum[wave] = inc;
+    __syncthreads();
+    int before = inc - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (w < wave) before += tt.wave_sum[w];
+        total += tt.wave_sum[w];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int g = 4 * threadIdx.x + i;
+        tt.end[g] = g < p.G ? before + cnt[i] : INT_MAX;
+    }
+    __syncthreads();
+    return total;
+}
+
+// Tile number v of the launch in the order of resolve_tile: an expert's tiles
+// together, its row tiles fastest.  Every wave searches by itself (64 lanes over
+// 16 entries each, then over those 16).
+__device__ __forceinline__ Tile find_tile(const TileTable &tt, int v, int tiles_n, int bm) {
+    const int lane = threadIdx.x & 63;
+    const int mt = v / tiles_n;
+    const int blk = __popcll(__ballot(tt.end[16 * lane + 15] <= mt));
+    const int g = 16 * blk + __popcll(__ballot(lane < 16 && tt.end[16 * blk + (lane & 15)] <= mt));
+    const int first = g > 0 ? tt.end[g - 1] : 0, n = tt.end[g] - first;
+    const int local = v - first * tiles_n;
     Tile t;
-    if (!resolve_tile<BM, BN>(p.g, &t, blockIdx.x, gridDim.x)) return;
-    const int N = p.g.N, K = p.K, kb = (K + 127) / 128;
-    const int m0 = t.m0, n0 = t.nt * BN;
+    t.g = __builtin_amdgcn_readfirstlane(g);
+    t.m0 = __builtin_amdgcn_readfirstlane((local % n) * bm);
+    t.nt = __builtin_amdgcn_readfirstlane(local / n);
+    const int lo = __builtin_amdgcn_readfirstlane(tt.lo[g]);
+    t.base = lo;
+    t.Mg = __builtin_amdgcn_readfirstlane(tt.hi[g]) - lo;
+    t.Kg = 0;
+    return t;
+}
+
+// Many rows per expert: 256 x 256 results a tile (NB = 2: 128 columns of W1 and
+// the same of W3), four waves of 128 x 128, one block per compute unit that
+// takes one tile after another.  Both operands come into two slots of shared
+// memory by direct loads, 128 bytes of K a slot, with the swizzle of the bf16
+// products (a 16-byte chunk here is 16 elements instead of 8); the scale dwords
+// of the same 128 of K come the same way.  Wave tiles this wide are what the
+// rates ask for: per 64 of K a wave reads 16 KiB from shared memory for 16
+// products of 64 cycles.  Slots of 128 bytes of K let each load ask L2 for whole
+// lines (with 64 bytes and four slots: twice the requests).
+//
+// A block of 128 of K is two steps of 64.  Step 0 multiplies fragments that are
+// in registers while those of step 1 are read; a barrier in its middle then
+// frees the slot, and the loads of two blocks ahead go out, spread over both
+// steps.  Step 1 starts with the wait and barrier for the next block, whose
+// first fragments are read under its products.  The next tile's first two
+// blocks are loaded under the last two of this one, and results leave from the
+// registers without shared memory, so that a tile's end costs its arithmetic
+// and the issue of its stores only.
+template <int NB, bool MAP>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx8_tile_kernel(Mx8Args p) {
+    constexpr int BM = 256, BN = 256 / NB, WGN = 2, NW = 4, S = 2;
+    constexpr int WTM = 128, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32, TT = NB * TN;
+    static_assert(TM == 4 && TT == 4, "sixteen 32 x 32 results a wave");
+    constexpr int kABytes = BM * 128, kBBytes = BN * 128, kStage = kABytes + NB * kBBytes;
+    constexpr int kL = kStage / (NW * 1024);  // operand loads of a wave per block
+    static_assert(kL == 16, "seven in step 0, nine in step 1");
+    constexpr int kScales = 512 * 4;          // scale dwords of 256 + 256 rows
+    constexpr int kRing = S * kStage;
+    static_assert(kRing + S * kScales + sizeof(TileTable) <= 160 * 1024, "one block per compute unit");
+    __shared__ __align__(1024) char smem[kRing + S * kScales];
+    __shared__ TileTable tt;
+
+    const int N = p.g.N, K = p.K, kb = (K + 127) / 128, kbe = max(kb, 2);  // blocks, two at least
+    const int tiles_n = (N + BN - 1) / BN;
+    const int tiles = build_table<BM>(p.g, tt) * tiles_n;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WGN, wn = wave % WGN, half = lane >> 5;
     const uint32_t sbase = __builtin_amdgcn_readfirstlane(lds_addr(smem));
-    const bool wact = m0 + wm * WTM < t.Mg && n0 + wn * WTN < N;
-    const int total = (K + 63) / 64;
+    int v = blockIdx.x;
+    if (v >= tiles) return;
+    Tile t = find_tile(tt, xcd_tile_order(v, tiles), tiles_n, BM);
 
-    // operand loads: rows past the group's or N, and K's end, load zeros
-    PA pa;
-    PB pb;
-    __amdgpu_buffer_rsrc_t ra, rb[NB];
-    const int32_t *map = p.map ? p.map + t.base + m0 : nullptr;
-    if (map) {
-        pa.init_mapped(wave, lane, K / 2, map, t.Mg - m0, K / 2);
+    // Operand loads: load i of wave w fills tile rows 32 i + 8 w .. + 7, lane l
+    // the chunk l % 8 of row 8 w + l / 8, which holds the row's chunk c (the
+    // swizzle goes by the row modulo 16, so c is the same for all i).  A buffer
+    // spans the tile's rows (MAP: all rows of a), so a lane's offset is its
+    // row's, the block's k goes into the scalar offset, and rows past the
+    // group's end or N are out of range and load zeros; so do offsets with bit 31
+    // set: ids outside the rows and, in the last block, chunks past K.
+    constexpr uint32_t kOut = 0x80000000u;
+    const int lrow = 8 * wave + (lane >> 3), c16 = 16 * ((lane & 7) ^ swz_kc(lrow, 8));
+    const uint32_t boff = static_cast<uint32_t>(lrow * K + c16), step32 = 32u * static_cast<uint32_t>(K);
+    struct Source {  // what the loads of a tile need
+        __amdgpu_buffer_rsrc_t a, b0, b1, as, bs;
+        uint32_t aoff[MAP ? 8 : 1], as_off, bs_off;
+    };
+    auto source = [&](const Tile &u) {
+        Source q;
+        const int rows = u.Mg - u.m0, n0 = u.nt * BN;
+        const int64_t r0 = u.base + u.m0;
+        const int m = 64 * wave + lane;  // scales: wave w takes rows 64 w .. + 63 of A's 256 and of B's
+        q.as_off = m < rows ? 4u * m : kOut;
+        if constexpr (MAP) {
+            auto id_of = [&](int mm) {
+                const int id = mm < rows ? p.map[r0 + mm] : -1;
+                return id >= 0 && id < p.a_rows ? id : -1;
+            };
 #pragma unroll
-        for (int i = 0; i < PA::kN; ++i) {  // ids outside the rows: zeros
-            const int row = ((i * NW + wave) * 1024 + lane * 16) / PA::kRowBytes;
-            const int id = row < t.Mg - m0 ? map[row] : 0;
-            if (id < 0 || id >= p.a_rows) pa.lim[i] = INT_MIN;
-        }
-        ra = make_rsrc(p.a, p.a_rows * K);
-    } else {
-        pa.init(wave, lane, K / 2, 0, t.Mg - m0, K / 2);
-        ra = make_rsrc(p.a + (t.base + m0) * K, static_cast<int64_t>(t.Mg - m0) * K);
-    }
-    pb.init(wave, lane, K / 2, 0, N - n0, K / 2);
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-        rb[b] = make_rsrc((b ? p.b1 : p.b0) + (static_cast<int64_t>(t.g) * N + n0) * K, static_cast<int64_t>(N - n0) * K);
-    // scale loads: wave w takes rows 64 w .. 64 w + 63 of A's 256 and of B's (of W1 and W3: 128 each)
-    int as_off = kOob, bs_off = kOob;
-    {
-        const int row = 64 * wave + lane;
-        if (row < t.Mg - m0) {
-            const int64_t id = map ? map[row] : t.base + m0 + row;
-            if (id >= 0 && id < p.a_rows) as_off = static_cast<int>(map ? id * 4 : row * 4);
-        }
-        const int col = NB == 2 ? row & 127 : row;
-        if (n0 + col < N) bs_off = col * 4;
-    }
-    const int64_t as_first = map ? 0 : t.base + m0;
-    const uint8_t *bsrc = (NB == 2 && wave >= 2) ? p.b1s : p.b0s;
-
-    auto issue_part = [&](int st, int part) {  // operand load `part` of slot st
-        const bool live = st < total;
-        const int kc = live ? st * 32 : INT_MAX, kadd = st * 64;
-        const uint32_t dst = sbase + (st & (S - 1)) * kStage;
-        if (part < PA::kN) {
-            pa.issue(ra, kc, kadd, dst, wave, part);
+            for (int i = 0; i < 8; ++i) {
+                const int id = id_of(32 * i + lrow);
+                q.aoff[i] = id >= 0 ? static_cast<uint32_t>(id) * static_cast<uint32_t>(K) + c16 : kOut;
+            }
+            const int id = id_of(m);
+            q.as_off = id >= 0 ? 4u * id : kOut;
+            q.a = make_rsrc(p.a, p.a_rows * K);
+            q.as = make_rsrc(p.as, p.a_rows * kb * 4);
         } else {
-            const int b = (part - PA::kN) / PB::kN, i = (part - PA::kN) % PB::kN;
-            pb.issue(rb[b], kc, kadd, dst + kABytes + b * kBBytes, wave, i);
+            q.a = make_rsrc(p.a + r0 * K, static_cast<int64_t>(min(rows, BM)) * K);
+            q.as = make_rsrc(p.as + r0 * 4, (p.a_rows * kb - r0) * 4);
+        }
+        const int64_t b_at = (static_cast<int64_t>(u.g) * N + n0) * K;
+        const int64_t bbytes = static_cast<int64_t>(min(N - n0, BN)) * K;
+        q.b0 = make_rsrc(p.b0 + b_at, bbytes);
+        q.b1 = make_rsrc((NB == 2 ? p.b1 : p.b0) + b_at, bbytes);
+        const int col = NB == 2 ? m & 127 : m;  // B's: of W1 and W3 128 each
+        q.bs_off = n0 + col < N ? 4u * col : kOut;
+        const int64_t bs_at = static_cast<int64_t>(u.g) * kb * N + n0;
+        q.bs = make_rsrc(((NB == 2 && wave >= 2) ? p.b1s : p.b0s) + bs_at * 4, (static_cast<int64_t>(kb) * N - n0) * 4);
+        return q;
+    };
+    // blocks past the end load zeros, so that the count of loads in flight stays the same
+    struct Plan {
+        uint32_t k, as, bs;  // scalar offsets of the block
+        uint32_t row;        // offset of this lane's chunk in the tile's first rows
+        uint32_t out;        // bit 31 set in lanes whose chunk is past K
+        uint32_t sout;       // bit 31 set where the block has no scales
+    };
+    auto plan = [&](int blk, bool live) {
+        live = live && blk < kb;
+        const uint32_t g = live ? blk : 0;
+        Plan q;
+        q.k = g * 128u;
+        q.as = g * static_cast<uint32_t>(p.a_rows) * 4u;
+        q.bs = g * static_cast<uint32_t>(N) * 4u;
+        q.row = fresh(boff);
+        q.out = live && static_cast<int>(q.k) + c16 < K ? 0u : kOut;
+        q.sout = live ? 0u : kOut;
+        return q;
+    };
+    auto issue_part = [&](const Source &c, const Plan &q, int slot, int part) {
+        const uint32_t dst = sbase + slot * kStage + wave * 1024;
+        if (part < 8) {
+            lds_dma16(c.a, (MAP ? c.aoff[MAP ? part : 0] : q.row + part * step32) | q.out, q.k, dst + part * 4096);
+        } else {
+            const int b = (part - 8) / (8 / NB), i = (part - 8) % (8 / NB);
+            lds_dma16(b ? c.b1 : c.b0, (q.row + i * step32) | q.out, q.k, dst + kABytes + b * kBBytes + i * 4096);
         }
     };
-    auto issue_scales = [&](int st) {  // even slots: the scales of their 128 of K
-        const bool live = st < total;
-        const int64_t g = live ? st >> 1 : 0;
-        const uint32_t dst = sbase + kRing + ((st >> 1) & (kScaleSlots - 1)) * kScales + wave * 256;
-        const __amdgpu_buffer_rsrc_t rsa = make_rsrc(p.as + (g * p.a_rows + as_first) * 4, (p.a_rows - as_first) * 4);
-        const __amdgpu_buffer_rsrc_t rsb = make_rsrc(bsrc + ((static_cast<int64_t>(t.g) * kb + g) * N + n0) * 4,
-                                                     static_cast<int64_t>(N - n0) * 4);
-        lds_dma4(rsa, live ? as_off : kOob, dst);
-        lds_dma4(rsb, live ? bs_off : kOob, dst + 1024);
+    auto issue_scales = [&](const Source &c, const Plan &q, int slot) {
+        const uint32_t dst = sbase + kRing + slot * kScales + wave * 256;
+        lds_dma4(c.as, c.as_off | q.sout, q.as, dst);
+        lds_dma4(c.bs, c.bs_off | q.sout, q.bs, dst + 1024);
     };
 
+    // fragment addresses: of the eight chunks of row l % 32, lane l reads chunks
+    // 4 s + l / 32 and 4 s + 2 + l / 32 in step s (the swizzle goes by the row
+    // modulo 32, so whole 32-row blocks are immediates)
+    const int row = lane & 31, sw = swz_kc(row, 8);
+    uint32_t fad[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) fad[c] = row * 128 + 16 * ((2 * c + half) ^ sw);
     f32x16_t acc[NB][TM][TN];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[b][i][j][r] = 0.0f;
-
-    // fragment addresses: lane l reads chunks l / 32 and 2 + l / 32 of row l % 32
-    // (the swizzle goes by the row modulo 32, so whole 32-row blocks are immediates)
-    const int row = lane & 31, sw = swz_kc(row, 4);
-    const uint32_t flo = row * 64 + 16 * (half ^ sw), fhi = row * 64 + 16 * ((2 + half) ^ sw);
     i32x8_t fA[2][TM], fB[2][TT];
     int sA[2][TM], sB[2][TT];
     typedef __attribute__((address_space(3))) const i32x4_t lds_i32x4;
-    auto frag = [&](uint32_t tile) {
-        const i32x4_t lo = *reinterpret_cast<lds_i32x4 *>(static_cast<uintptr_t>(tile + flo));
-        const i32x4_t hi = *reinterpret_cast<lds_i32x4 *>(static_cast<uintptr_t>(tile + fhi));
-        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    struct Frags {  // addresses of a step's fragments: one add each, the rest immediates
+        uint32_t alo, ahi, blo, bhi;
     };
-    auto read_unit = [&](int set, int st, int u) {
-        const uint32_t sa = sbase + (st & (S - 1)) * kStage;
-        if (u < TM) {
-            fA[set][u] = frag(sa + (wm * WTM + 32 * u) * 64);
-        } else {
-            const int b = (u - TM) / TN, j = (u - TM) % TN;
-            fB[set][u - TM] = frag(sa + kABytes + b * kBBytes + (wn * WTN + 32 * j) * 64);
-        }
+    auto frags = [&](int s, int slot) {
+        const uint32_t sa = sbase + slot * kStage + wm * WTM * 128;
+        const uint32_t sb = sbase + slot * kStage + kABytes + wn * WTN * 128;
+        return Frags{fresh(sa + fad[2 * s]), fresh(sa + fad[2 * s + 1]), fresh(sb + fad[2 * s]), fresh(sb + fad[2 * s + 1])};
     };
-    auto read_scales = [&](int set, int st) {  // the scales of slot st's 128 of K
-        const uint32_t ss = sbase + kRing + ((st >> 1) & (kScaleSlots - 1)) * kScales;
+    auto read_unit = [&](const Frags &f, int s, int u) {  // fragment u of step s
+        const uint32_t off = u < TM ? 32 * u * 128 : ((u - TM) / TN) * kBBytes + 32 * ((u - TM) % TN) * 128;
+        const i32x4_t lo = *reinterpret_cast<lds_i32x4 *>(static_cast<uintptr_t>((u < TM ? f.alo : f.blo) + off));
+        const i32x4_t hi = *reinterpret_cast<lds_i32x4 *>(static_cast<uintptr_t>((u < TM ? f.ahi : f.bhi) + off));
+        const i32x8_t v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        if (u < TM) fA[s][u] = v;
+        else fB[s][u - TM] = v;
+    };
+    auto read_scales = [&](int set, int slot) {
+        const uint32_t ss = sbase + kRing + slot * kScales;
+        const uint32_t sa = fresh(ss + (wm * WTM + row) * 4), sb = fresh(ss + 1024 + (wn * WTN + row) * 4);
 #pragma unroll
-        for (int i = 0; i < TM; ++i) sA[set][i] = lds_read_i32(ss + (wm * WTM + 32 * i + row) * 4) >> (8 * half);
+        for (int i = 0; i < TM; ++i) sA[set][i] = lds_read_i32(sa + 128 * i) >> (8 * half);
 #pragma unroll
-        for (int u = 0; u < TT; ++u)
-            sB[set][u] = lds_read_i32(ss + 1024 + ((u / TN) * BN + wn * WTN + 32 * (u % TN) + row) * 4) >> (8 * half);
+        for (int u = 0; u < TT; ++u) sB[set][u] = lds_read_i32(sb + 4 * (u / TN) * BN + 128 * (u % TN)) >> (8 * half);
+    };
+    auto read_first = [&](int slot) {
+        read_scales(0, slot);
+        const Frags f = frags(0, slot);
+#pragma unroll
+        for (int u = 0; u < TM + TT; ++u) read_unit(f, 0, u);
     };
 
+    Source src = source(t);
 #pragma unroll
-    for (int st = 0; st < S; ++st) {
-        if (st % 2 == 0) issue_scales(st);
+    for (int blk = 0; blk < S; ++blk) {
+        const Plan pl = plan(blk, true);
+        issue_scales(src, pl, blk);
 #pragma unroll
-        for (int u = 0; u < kL; ++u) issue_part(st, u);
+        for (int u = 0; u < kL; ++u) issue_part(src, pl, blk, u);
     }
-    wait_vmem<3 * kL + 2>();  // slot 0 has landed (slot 2 brings scales too)
+    wait_vmem<kL + 2>();  // block 0 has landed
     __syncthreads();
-    auto k_loop = [&](auto active) {
-        constexpr bool ACT = decltype(active)::value;
-        if constexpr (ACT) {
-            read_scales(0, 0);
+    int slot = 0;
+    while (true) {
+        const int nv = v + static_cast<int>(gridDim.x);
+        const bool more = nv < tiles;
+        const Tile next = more ? find_tile(tt, xcd_tile_order(nv, tiles), tiles_n, BM) : t;
+        const Source nsrc = source(next);
+        const int m0 = t.m0, n0 = t.nt * BN;
+        read_first(slot);
 #pragma unroll
-            for (int u = 0; u < TM + TT; ++u) read_unit(0, 0, u);
-        }
-        // P: parity of the slot; Q: of its 128 of K (register sets)
-        auto step = [&](int it, auto par, auto grp) {
-            constexpr int P = decltype(par)::value, Q = decltype(grp)::value;
-            wait_vmem<2 * kL + 2>();  // slots it + 2 and it + 3 may be in flight
-            __syncthreads();
-            if constexpr (P == 0) issue_scales(it + S);
-            if constexpr (ACT && P == 1) read_scales(Q ^ 1, it + 1);
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int q = 0; q < TM * TT; ++q) {
-                const int u = q / TM, i = q % TM;
-                if constexpr (ACT) {
-                    if (q < TM + TT) read_unit(P ^ 1, it + 1, q);
-                    acc[u / TN][i][u % TN] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                        fB[P][u], fA[P][i], acc[u / TN][i][u % TN], 0, 0, 2 * P, sB[Q][u], 2 * P, sA[Q][i]);
-                }
-                if (q % 2 == 0 && q / 2 < kL) issue_part(it + S, q / 2);
-            }
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[b][i][j][r] = 0.0f;
+        // product q of step s.  The order around it is pinned: left to itself
+        // the compiler puts all reads in front of the products, which then
+        // wait for shared memory.
+        auto product = [&](int s, int q) {
+            const int u = q / TM, i = q % TM;
+            if (s == 0)
+                acc[u / TN][i][u % TN] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    fB[0][u], fA[0][i], acc[u / TN][i][u % TN], 0, 0, 0, sB[0][u], 0, sA[0][i]);
+            else
+                acc[u / TN][i][u % TN] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    fB[1][u], fA[1][i], acc[u / TN][i][u % TN], 0, 0, 2, sB[0][u], 2, sA[0][i]);
         };
-        constexpr std::integral_constant<int, 0> c0{};
-        constexpr std::integral_constant<int, 1> c1{};
-        for (int it = 0; it < total; it += 4) {
-            step(it, c0, c0);
-            if (it + 1 < total) step(it + 1, c1, c0);
-            if (it + 2 < total) step(it + 2, c0, c1);
-            if (it + 3 < total) step(it + 3, c1, c1);
-        }
-    };
-    if (wact) k_loop(std::true_type{});
-    else k_loop(std::false_type{});
-    wait_vmem<0>();  // no load may still target the ring
-    if constexpr (NB == 1) {
-        GroupPtrs<bf16_t> q{};
-        q.crow = t.base;
-        gemm_epilogue<BM, BN, WGM, WGN, 1, kRing, EPI_STORE, bf16_t>(p.g, t, q, acc, smem, sbase, m0, n0, lane, wave);
-    } else {
-        // lane l: row 32 i + l % 32, columns 32 j + 8 g + 4 (l / 32) + r; a block of
-        // 32 columns lies in lanes l and l ^ 32.  The bytes leave through the ring
-        // (rows of 144 bytes), 16 at a time, a row's four scale bytes as one dword.
-        constexpr int LDC = BN + 16;
-        char *const sc = smem + BM * LDC;
-        static_assert(BM * LDC + BM * 4 <= kRing, "staging");
-        __syncthreads();
+        for (int blk = 0; blk < kbe; ++blk) {
+            const bool ahead = blk + 2 >= kbe;  // the loads are the next tile's first two blocks
+            if (blk + 2 == kbe) src = nsrc;
+            const Plan pl = plan(ahead ? blk + 2 - kbe : blk + 2, !ahead || more);
+            const Frags f1 = frags(1, slot);
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                float o[16];
-                uint32_t a = 0u;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float h1 = acc[0][i][j][r];
-                    o[r] = h1 * __builtin_amdgcn_rcpf(1.0f + __expf(-h1)) * acc[1][i][j][r];
-                    a = max(a, __float_as_uint(o[r]) & 0x7fffffffu);
+            for (int q = 0; q < 16; ++q) {
+                product(0, q);
+                if (q < TM + TT) read_unit(f1, 1, q);
+                if (q == 8) {
+                    __syncthreads();  // every wave has read this block: its slot is free
+                    issue_scales(src, pl, slot);
                 }
-                a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), 32, 64)));
-                const uint32_t byte = mx8_scale_byte(a);
-                const float s = mx8_inv_scale(byte);
-                const int m = wm * WTM + 32 * i + row, c = wn * WTN + 32 * j;
-#pragma unroll
-                for (int r = 0; r < 16; r += 4)
-                    *reinterpret_cast<uint32_t *>(smem + m * LDC + c + 2 * r + 4 * half) =
-                        byte == 255u ? 0x7f7f7f7fu : mx8_pack4(o[r] * s, o[r + 1] * s, o[r + 2] * s, o[r + 3] * s);
-                // past N: the byte that fills the last group (a NaN row is NaN there too)
-                if (half == 0) sc[m * 4 + c / 32] = static_cast<char>(n0 + c < N ? byte : kMxOne);
+                if (q > 8) issue_part(src, pl, slot, q - 9);
+                __builtin_amdgcn_sched_barrier(0);
             }
-        __syncthreads();
-        const int rows = min(BM, t.Mg - m0);
-        for (int c = threadIdx.x; c < rows * (BN / 16); c += 256) {
-            const int m = c / (BN / 16), n = 16 * (c % (BN / 16));
-            if (n0 + n < N)
-                *reinterpret_cast<uint4 *>(p.q + (t.base + m0 + m) * N + n0 + n) =
-                    *reinterpret_cast<const uint4 *>(smem + m * LDC + n);
+            wait_vmem<2 + 7>();  // the next block has landed (what is out is of the one after)
+            __syncthreads();
+            read_scales(1, slot ^ 1);
+            const Frags f0 = frags(0, slot ^ 1);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                product(1, q);
+                if (q < TM + TT) read_unit(f0, 0, q);
+                if (q < 9) issue_part(src, pl, slot, q + 7);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                sA[0][i] = sA[1][i];
+                sB[0][i] = sB[1][i];
+            }
+            slot ^= 1;
         }
-        if (static_cast<int>(threadIdx.x) < rows)
-            *reinterpret_cast<uint32_t *>(p.qs + (static_cast<int64_t>(n0 / 128) * p.g.extent + t.base + m0 + threadIdx.x) * 4) =
-                *reinterpret_cast<const uint32_t *>(sc + 4 * threadIdx.x);
+        // the sums stay in the accumulation registers until their turn
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[b][i][j]));
+        // lane l: row 32 i + l % 32, columns 32 j + 8 g + 4 (l / 32) + r.  Swapping
+        // the lanes' halves gives each 16 consecutive bytes of its row.  Stores go
+        // through buffers that end with the group's rows and with bit 31 set past
+        // N, so that nothing branches and each result stays in its accumulator
+        // until its turn.
+        const int64_t r0 = t.base + m0;
+        const int rows = min(t.Mg - m0, BM);
+        typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+        const int erow = static_cast<int>(fresh(wm * WTM + row));
+        if constexpr (NB == 1) {
+            const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.y + r0 * N, static_cast<int64_t>(rows) * N * 2);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const int c = n0 + wn * WTN + 32 * j;
+                    const uint32_t at = static_cast<uint32_t>((erow + 32 * i) * N + c + 8 * half) * 2u;
+#pragma unroll
+                    for (int g = 0; g < 4; g += 2) {
+                        const f32x16_t &a = acc[0][i][j];
+                        const auto x = __builtin_amdgcn_permlane32_swap(
+                            cvt_bf16x2(a[4 * g], a[4 * g + 1]), cvt_bf16x2(a[4 * g + 4], a[4 * g + 5]), false, false);
+                        const auto y = __builtin_amdgcn_permlane32_swap(
+                            cvt_bf16x2(a[4 * g + 2], a[4 * g + 3]), cvt_bf16x2(a[4 * g + 6], a[4 * g + 7]), false, false);
+                        __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{x[0], y[0], x[1], y[1]}, ry,
+                                                               static_cast<int>(c < N ? at + 16u * g : kOut), 0, 0);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);  // one 32 x 32 result at a time: registers
+                }
+        } else {
+            const __amdgpu_buffer_rsrc_t rq = make_rsrc(p.q + r0 * N, static_cast<int64_t>(rows) * N);
+            const __amdgpu_buffer_rsrc_t rs =
+                make_rsrc(p.qs + (static_cast<int64_t>(n0 / 128) * p.g.extent + r0) * 4, rows * 4);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int m = erow + 32 * i;
+                uint32_t bytes = 0u;
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const int c = n0 + wn * WTN + 32 * j;
+                    f32x16_t h1 = acc[0][i][j], h3 = acc[1][i][j];
+                    asm volatile("" : "+v"(h1), "+v"(h3));
+                    float o[16];
+                    uint32_t a = 0u;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        o[e] = h1[e] * __builtin_amdgcn_rcpf(1.0f + __expf(-h1[e])) * h3[e];
+                        a = max(a, __float_as_uint(o[e]) & 0x7fffffffu);
+                    }
+                    const auto other = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+                    a = max(other[0], other[1]);
+                    const uint32_t byte = mx8_scale_byte(a);
+                    const float s = mx8_inv_scale(byte);
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        w[e / 4] = mx8_pack4(o[e] * s, o[e + 1] * s, o[e + 2] * s, o[e + 3] * s);
+                    const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+                    const auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+                    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{x[0], x[1], y[0], y[1]}, rq,
+                                                           static_cast<int>(c < N ? m * N + c + 16 * half : kOut), 0, 0);
+                    // past N: the byte that fills the last group (a NaN row is NaN there too)
+                    bytes |= (c < N ? byte : kMxOne) << (8 * j);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(bytes), rs,
+                                                      static_cast<int>(half ? kOut : m * 4u + 2u * wn), 0, 0);
+            }
+        }
+        if (!more) break;
+        t = next;
+        v = nv;
     }
+    wait_vmem<0>();  // no load may still target the slots when the block ends
 }
 
-template <int NB>
+template <int NB, bool MAP>
 hipError_t launch_tile(const Mx8Args &p, hipStream_t s) {
     constexpr int BM = 256, BN = 256 / NB;
     const int64_t tiles = p.g.extent / BM + std::min<int64_t>(p.g.G, p.g.extent);
-    const int64_t grid = tiles * ((p.g.N + BN - 1) / BN);
+    const int64_t grid = std::min<int64_t>(tiles * ((p.g.N + BN - 1) / BN), kComputeUnits);
     if (grid <= 0) return hipSuccess;
-    hipLaunchKernelGGL((mx8_tile_kernel<NB, 4>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((mx8_tile_kernel<NB, MAP>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
@@ -570,7 +759,10 @@ template <int NB>
 hipError_t product(const Mx8Args &p, hipStream_t s) {
     // few rows per expert: the weights' bytes bound it
     if (p.g.extent <= 48 * static_cast<int64_t>(p.g.G)) return launch_stream<NB, 2, 8>(p, s);
-    return launch_tile<NB>(p, s);
+    if constexpr (NB == 2) {
+        if (p.map) return launch_tile<2, true>(p, s);
+    }
+    return launch_tile<NB, false>(p, s);
 }
 
 }  // namespace
@@ -638,8 +830,6 @@ hipError_t launch_ffn_down_mx8(const void *act, const void *act_scale, const voi
     p.b0 = static_cast<const uint8_t *>(w2);
     p.b0s = static_cast<const uint8_t *>(w2s);
     p.y = static_cast<bf16_t *>(ye);
-    p.g.C0 = ye;
-    p.g.ldc = d;
     return product<1>(p, s);
 }
 

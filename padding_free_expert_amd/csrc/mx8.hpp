@@ -27,14 +27,17 @@ constexpr uint32_t kMxOne = 127u;
 // clamped at 2^-127, where magnitudes below 448 * 2^-127 lose nothing but
 // range that fp32 holds as subnormals.
 __device__ __forceinline__ uint32_t mx8_scale_byte(uint32_t amax_bits) {
-    if (amax_bits >= 0x7f800000u) return 255u;
-    if (amax_bits == 0u) return kMxOne;
-    const int b = static_cast<int>(amax_bits >> 23) - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return static_cast<uint32_t>(b < 0 ? 0 : b);
+    const int e = static_cast<int>(amax_bits >> 23) - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    uint32_t b = static_cast<uint32_t>(max(e, 0));
+    b = amax_bits == 0u ? kMxOne : b;
+    return amax_bits >= 0x7f800000u ? 255u : b;
 }
 
-// 2^(127 - b): what the elements are multiplied by (b <= 247 in finite blocks)
-__device__ __forceinline__ float mx8_inv_scale(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+// 2^(127 - b), what the elements are multiplied by (b <= 247 in finite blocks);
+// a NaN for b = 255, so that every element becomes one
+__device__ __forceinline__ float mx8_inv_scale(uint32_t b) {
+    return __uint_as_float(b == 255u ? 0x7fc00000u : (254u - b) << 23);
+}
 
 // 2^(b - 127); b = 0 is fp32's subnormal 2^-127, b = 255 a NaN
 __device__ __forceinline__ float mx8_scale(uint32_t b) {
@@ -62,7 +65,7 @@ __device__ __forceinline__ uint32_t mx8_quant(const float (&f)[V], uint32_t (&ou
     const float s = mx8_inv_scale(b);
 #pragma unroll
     for (int i = 0; i < V; i += 4)
-        out[i / 4] = b == 255u ? 0x7f7f7f7fu : mx8_pack4(f[i] * s, f[i + 1] * s, f[i + 2] * s, f[i + 3] * s);
+        out[i / 4] = mx8_pack4(f[i] * s, f[i + 1] * s, f[i + 2] * s, f[i + 3] * s);
     return b;
 }
 
