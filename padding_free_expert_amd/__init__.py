@@ -594,22 +594,39 @@ def xmoe_scatter_rows(src, index, dst, n: Optional[int] = None, stream=None):
 _F8, _U8 = torch.float8_e4m3fn, torch.uint8
 
 
-def _one_device(*ts: Optional[torch.Tensor]):
+_HERE_ALREADY = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on_device(*ts: Optional[torch.Tensor]):
     """Context of the call's device (the library launches on the current one),
-    which all its tensors must share."""
-    ts = [t for t in ts if t is not None]
-    if any(t.device != ts[0].device for t in ts):
-        raise ValueError("the call's tensors are on different devices")
-    dev = ts[0].device
-    if not ts[0].is_cuda or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()  # host tensors are refused when their pointers are taken
+    which all its tensors must share.  A single token's call is bound by its
+    host time, so nothing is entered where the device is the current one
+    already (host tensors are refused when their pointers are taken)."""
+    dev = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("the call's tensors are on different devices")
+    if dev < 0 or dev == torch.cuda.current_device():
+        return _HERE_ALREADY
     return torch.cuda.device(dev)
 
 
-def _workspace(ws: Optional[torch.Tensor], need: int, like: torch.Tensor):
-    """(tensor, bytes): the caller's workspace, or one of `need` bytes."""
+def _stream_on(stream, like: torch.Tensor) -> int:
+    """The caller's stream, or the current one of the tensors' device."""
+    if stream is None and _raw_stream is not None and like.is_cuda:
+        return _raw_stream(like.get_device())
+    return _stream(stream)
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, like: torch.Tensor, stream=None):
+    """(tensor, bytes): the caller's workspace, or one of `need` bytes that torch
+    does not hand out again before the call's stream is done with it."""
     if ws is None:
         ws = torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+        if stream is not None and like.is_cuda:
+            ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(_stream(stream), device=like.device))
     return ws, ws.numel() * ws.element_size()
 
 
@@ -623,9 +640,9 @@ def xmoe_add_rmsnorm(x, res, gamma, eps: float, sum=None, y=None, q=None, scale=
     _shape(q, (T, d), "q", _F8)
     _shape(scale, mx8_scale_shape(T, d), "scale", _U8)
     _shape(rstd, (T,), "rstd", _F32)
-    with _one_device(x, res, gamma, sum, y, q, scale, rstd):
+    with _on_device(x, res, gamma, sum, y, q, scale, rstd):
         _check(_lib_norm(_ptr(x), _ptr(res), _ptr(gamma), _dt(x), T, d, eps, _ptr(sum), _ptr(y), _ptr(q), _ptr(scale),
-                         _ptr(rstd), _stream(stream)), "xmoe_add_rmsnorm")
+                         _ptr(rstd), _stream_on(stream, x)), "xmoe_add_rmsnorm")
 
 
 def xmoe_add_rmsnorm_bwd_workspace_size(T: int, d: int, dtype) -> int:
@@ -641,10 +658,10 @@ def xmoe_add_rmsnorm_bwd(dy, dsum, sum, gamma, rstd, dx, dgamma, workspace=None,
     _shape(gamma, (d,), "gamma", dy.dtype)
     _shape(rstd, (T,), "rstd", _F32)
     _shape(dgamma, (d,), "dgamma", _F32)
-    workspace, nbytes = _workspace(workspace, xmoe_add_rmsnorm_bwd_workspace_size(T, d, dy.dtype), dy)
-    with _one_device(dy, dsum, sum, gamma, rstd, dx, dgamma, workspace):
+    workspace, nbytes = _workspace(workspace, xmoe_add_rmsnorm_bwd_workspace_size(T, d, dy.dtype), dy, stream)
+    with _on_device(dy, dsum, sum, gamma, rstd, dx, dgamma, workspace):
         _check(_lib_norm_bwd(_ptr(dy), _ptr(dsum), _ptr(sum), _ptr(gamma), _ptr(rstd), _dt(dy), T, d, _ptr(dx),
-                             _ptr(dgamma), _ptr(workspace), nbytes, _stream(stream)), "xmoe_add_rmsnorm_bwd")
+                             _ptr(dgamma), _ptr(workspace), nbytes, _stream_on(stream, dy)), "xmoe_add_rmsnorm_bwd")
 
 
 def _sequences(logits, seq_offsets, token_mask, coef) -> int:
@@ -676,10 +693,10 @@ def xmoe_balance_loss(logits, topk_ids, alpha: float, loss, counts, coef, seq_of
     _shape(topk_ids, (T, k), "topk_ids", _I32)
     _shape(loss, (1,), "loss", _F32)
     _shape(counts, (n_seq, E), "counts", _I32)
-    workspace, nbytes = _workspace(workspace, xmoe_balance_loss_workspace_size(T, E, n_seq), logits)
-    with _one_device(logits, topk_ids, loss, counts, coef, seq_offsets, token_mask, workspace):
+    workspace, nbytes = _workspace(workspace, xmoe_balance_loss_workspace_size(T, E, n_seq), logits, stream)
+    with _on_device(logits, topk_ids, loss, counts, coef, seq_offsets, token_mask, workspace):
         _check(_lib_balance(_ptr(logits), _ptr(topk_ids), T, E, k, _ptr(seq_offsets), n_seq, _ptr(token_mask), alpha,
-                            _ptr(loss), _ptr(counts), _ptr(coef), _ptr(workspace), nbytes, _stream(stream)),
+                            _ptr(loss), _ptr(counts), _ptr(coef), _ptr(workspace), nbytes, _stream_on(stream, logits)),
                "xmoe_balance_loss")
 
 
@@ -690,9 +707,9 @@ def xmoe_balance_loss_bwd(logits, coef, dlogits, seq_offsets=None, token_mask=No
     n_seq = _sequences(logits, seq_offsets, token_mask, coef)
     _shape(dlogits, (T, E), "dlogits", _F32)
     _shape(dloss, (1,), "dloss", _F32)
-    with _one_device(logits, coef, dlogits, seq_offsets, token_mask, dloss):
+    with _on_device(logits, coef, dlogits, seq_offsets, token_mask, dloss):
         _check(_lib_balance_bwd(_ptr(logits), _ptr(coef), T, E, _ptr(seq_offsets), n_seq, _ptr(token_mask),
-                                _ptr(dloss), _ptr(dlogits), _stream(stream)), "xmoe_balance_loss_bwd")
+                                _ptr(dloss), _ptr(dlogits), _stream_on(stream, logits)), "xmoe_balance_loss_bwd")
 
 
 def xmoe_route_bwd_balance(x, wg, logits, topk_ids, dtopk_w, coef, dx, dwg, workspace, inv_temperature: float = 1.0,
@@ -711,12 +728,12 @@ def xmoe_route_bwd_balance(x, wg, logits, topk_ids, dtopk_w, coef, dx, dwg, work
     _shape(dx, (T, d), "dx", x.dtype)
     _shape(dwg, (d, E), "dwg", _F32)
     _shape(dloss, (1,), "dloss", _F32)
-    with _one_device(x, wg, logits, topk_ids, dtopk_w, coef, dx, dwg, workspace, seq_offsets, token_mask, dloss):
+    with _on_device(x, wg, logits, topk_ids, dtopk_w, coef, dx, dwg, workspace, seq_offsets, token_mask, dloss):
         _check(_lib_rbwd_balance(_ptr(x), _ptr(wg), _ptr(logits), _ptr(topk_ids), dtopk_w.data_ptr(),
                                  dtopk_w.stride(0), _ptr(coef),
                                  _ptr(seq_offsets), n_seq, _ptr(token_mask), _ptr(dloss), _dt(x), T, d, E, k,
                                  inv_temperature, int(bool(accumulate)), _ptr(dx), _ptr(dwg), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), _stream(stream)),
+                                 workspace.numel() * workspace.element_size(), _stream_on(stream, x)),
                "xmoe_route_bwd_balance")
 
 
@@ -730,8 +747,8 @@ def xmoe_mx8_quantize(x, q, scale, stream=None):
     n, K = x.shape
     _shape(q, (n, K), "q", _F8)
     _shape(scale, mx8_scale_shape(n, K), "scale", _U8)
-    with _one_device(x, q, scale):
-        _check(_lib_mx8_q(_ptr(x), _dt(x), n, K, _ptr(q), _ptr(scale), _stream(stream)), "xmoe_mx8_quantize")
+    with _on_device(x, q, scale):
+        _check(_lib_mx8_q(_ptr(x), _dt(x), n, K, _ptr(q), _ptr(scale), _stream_on(stream, x)), "xmoe_mx8_quantize")
 
 
 def xmoe_mx8_dequantize(q, scale, out, stream=None):
@@ -739,8 +756,8 @@ def xmoe_mx8_dequantize(q, scale, out, stream=None):
     n, K = out.shape
     _shape(q, (n, K), "q", _F8)
     _shape(scale, mx8_scale_shape(n, K), "scale", _U8)
-    with _one_device(q, scale, out):
-        _check(_lib_mx8_dq(_ptr(q), _ptr(scale), _dt(out), n, K, _ptr(out), _stream(stream)), "xmoe_mx8_dequantize")
+    with _on_device(q, scale, out):
+        _check(_lib_mx8_dq(_ptr(q), _ptr(scale), _dt(out), n, K, _ptr(out), _stream_on(stream, q)), "xmoe_mx8_dequantize")
 
 
 def xmoe_mx8_quantize_weights(w, q, scale, stream=None):
@@ -749,8 +766,8 @@ def xmoe_mx8_quantize_weights(w, q, scale, stream=None):
     E, K, N = w.shape
     _shape(q, (E, N, K), "q", _F8)
     _shape(scale, (E,) + mx8_scale_shape(N, K), "scale", _U8)
-    with _one_device(w, q, scale):
-        _check(_lib_mx8_qw(_ptr(w), _dt(w), E, K, N, _ptr(q), _ptr(scale), _stream(stream)),
+    with _on_device(w, q, scale):
+        _check(_lib_mx8_qw(_ptr(w), _dt(w), E, K, N, _ptr(q), _ptr(scale), _stream_on(stream, w)),
                "xmoe_mx8_quantize_weights")
 
 
@@ -770,10 +787,10 @@ def xmoe_expert_ffn_up_mx8(xq, xscale, w1, w1_scale, w3, w3_scale, expert_offset
     _shape(act, (rows, h), "act", _F8)
     _shape(act_scale, mx8_scale_shape(rows, h), "act_scale", _U8)
     _shape(token_ids, (rows,), "token_ids", _I32)
-    with _one_device(xq, xscale, w1, w1_scale, w3, w3_scale, expert_offsets, act, act_scale, token_ids):
+    with _on_device(xq, xscale, w1, w1_scale, w3, w3_scale, expert_offsets, act, act_scale, token_ids):
         _check(_lib_up8(_ptr(xq), _ptr(xscale), _ptr(token_ids), T, _ptr(w1), _ptr(w1_scale), _ptr(w3),
                         _ptr(w3_scale), _ptr(expert_offsets), E, rows, d, h, _ptr(act), _ptr(act_scale),
-                        _stream(stream)), "xmoe_expert_ffn_up_mx8")
+                        _stream_on(stream, xq)), "xmoe_expert_ffn_up_mx8")
 
 
 def xmoe_expert_ffn_down_mx8(act, act_scale, w2, w2_scale, expert_offsets, ye, stream=None):
@@ -786,6 +803,6 @@ def xmoe_expert_ffn_down_mx8(act, act_scale, w2, w2_scale, expert_offsets, ye, s
     _shape(w2_scale, (E,) + mx8_scale_shape(d, h), "w2_scale", _U8)
     _shape(expert_offsets, (E + 1,), "expert_offsets", _I32)
     _shape(ye, (rows, d), "ye", torch.bfloat16)
-    with _one_device(act, act_scale, w2, w2_scale, expert_offsets, ye):
+    with _on_device(act, act_scale, w2, w2_scale, expert_offsets, ye):
         _check(_lib_down8(_ptr(act), _ptr(act_scale), _ptr(w2), _ptr(w2_scale), _ptr(expert_offsets), E, rows, d, h,
-                          _ptr(ye), _stream(stream)), "xmoe_expert_ffn_down_mx8")
+                          _ptr(ye), _stream_on(stream, act)), "xmoe_expert_ffn_down_mx8")

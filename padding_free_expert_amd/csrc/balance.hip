@@ -12,11 +12,10 @@
 // a chunk of tokens and the sums and counts of each sequence's piece of it.
 // Piece (chunk b, sequence s) has row b + s of the partial sums: chunks and
 // sequences both only go forward, so no two pieces share a row and the rows
-// number at most chunks + S.  A second kernel, one block per sequence, adds a
-// sequence's rows in order and writes counts and coef; its last block to end
-// adds the sequences' losses in order.  Nothing depends on the order in which
-// blocks run.  Memory-bound: the logits are read once here, once in the
-// backward, which writes the gradient.
+// number at most chunks + S.  A second kernel adds a sequence's rows in order and
+// writes counts and coef; its last block to end adds the blocks' losses in
+// order.  Nothing depends on the order in which blocks run.  Memory-bound: the
+// logits are read once here, once in the backward, which writes the gradient.
 #include <algorithm>
 
 #include "balance.hpp"
@@ -29,19 +28,23 @@ namespace {
 
 constexpr int kWaves = 4;
 
-// Tokens per block: about 512 blocks, at least one step of every wave
+// Tokens per block: about 1024 blocks, four on each compute unit, at least one
+// step of every wave; at most 128, so that a sum of p has few terms in sequence
 inline int chunk_tokens(int64_t T) {
     int c = 16;
-    while (c < 128 && T > static_cast<int64_t>(c) * 512) c *= 2;
+    while (c < 128 && T > static_cast<int64_t>(c) * 1024) c *= 2;
     return c;
 }
+// experts per block of the second kernel: its 32 row groups share a sequence's rows
+constexpr int kFinalExperts = 32;
+inline int final_blocks(int E) { return (E + kFinalExperts - 1) / kFinalExperts; }
 inline size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 struct BalanceWs {
     float *psum;      // [rows, E]
     int32_t *csum;    // [rows, E]
     int32_t *nsum;    // [rows]
-    double *seq_loss; // [S]
+    double *part_loss; // [S, blocks of experts]
     int32_t *ticket;  // [1]
     size_t bytes;
 };
@@ -58,34 +61,38 @@ BalanceWs balance_ws(void *ws, int64_t T, int E, int S) {
     b.psum = reinterpret_cast<float *>(take(rows * E * 4));
     b.csum = reinterpret_cast<int32_t *>(take(rows * E * 4));
     b.nsum = reinterpret_cast<int32_t *>(take(rows * 4));
-    b.seq_loss = reinterpret_cast<double *>(take(static_cast<size_t>(S) * 8));
+    b.part_loss = reinterpret_cast<double *>(take(static_cast<size_t>(S) * final_blocks(E) * 8));
     b.ticket = reinterpret_cast<int32_t *>(take(4));
     b.bytes = at;
     return b;
 }
 
-// Probabilities of one token in its LT lanes: lane r holds QQ experts, the
-// 16-byte chunks r, r + LT, ... of the row (expert of value q: 4 (r + LT (q / 4))
-// + q % 4).  Experts past E and dead tokens hold 0.
+// One token's logits in its LT lanes: lane r holds QQ experts, the 16-byte chunks
+// r, r + LT, ... of the row (expert of value q: 4 (r + LT (q / 4)) + q % 4).
+// Experts past E and dead tokens hold -infinity.
 template <int LT, int QQ>
-__device__ __forceinline__ void token_softmax(const float *row, bool live, int r, int E, float (&p)[QQ]) {
+__device__ __forceinline__ void load_token(const float *row, bool live, int r, int E, float (&p)[QQ]) {
     auto ex = [&](int q) { return 4 * (r + LT * (q >> 2)) + (q & 3); };
 #pragma unroll
     for (int q = 0; q < QQ; ++q) p[q] = -INFINITY;
-    if (live) {
-        if (E % 4 == 0) {
+    if (!live) return;
+    if (E % 4 == 0) {
 #pragma unroll
-            for (int q = 0; q < QQ; q += 4)
-                if (ex(q) < E) {
-                    const float4 v = *reinterpret_cast<const float4 *>(row + ex(q));
-                    p[q] = v.x; p[q + 1] = v.y; p[q + 2] = v.z; p[q + 3] = v.w;
-                }
-        } else {
+        for (int q = 0; q < QQ; q += 4)
+            if (ex(q) < E) {
+                const float4 v = *reinterpret_cast<const float4 *>(row + ex(q));
+                p[q] = v.x; p[q + 1] = v.y; p[q + 2] = v.z; p[q + 3] = v.w;
+            }
+    } else {
 #pragma unroll
-            for (int q = 0; q < QQ; ++q)
-                if (ex(q) < E) p[q] = row[ex(q)];
-        }
+        for (int q = 0; q < QQ; ++q)
+            if (ex(q) < E) p[q] = row[ex(q)];
     }
+}
+
+// Logits -> probabilities in place (dead tokens: 0).  One division a token.
+template <int LT, int QQ>
+__device__ __forceinline__ void token_softmax(bool live, int r, int E, float (&p)[QQ]) {
     float mx = -INFINITY;
 #pragma unroll
     for (int q = 0; q < QQ; ++q) mx = fmaxf(mx, p[q]);
@@ -94,13 +101,14 @@ __device__ __forceinline__ void token_softmax(const float *row, bool live, int r
     float den = 0.0f;
 #pragma unroll
     for (int q = 0; q < QQ; ++q) {
-        p[q] = ex(q) < E && live ? expf(p[q] - mx) : 0.0f;
+        p[q] = 4 * (r + LT * (q >> 2)) + (q & 3) < E && live ? expf(p[q] - mx) : 0.0f;
         den += p[q];
     }
 #pragma unroll
     for (int off = LT / 2; off > 0; off >>= 1) den += __shfl_xor(den, off, 64);
+    const float inv = 1.0f / den;
 #pragma unroll
-    for (int q = 0; q < QQ; ++q) p[q] = live ? p[q] / den : 0.0f;
+    for (int q = 0; q < QQ; ++q) p[q] = live ? p[q] * inv : 0.0f;
 }
 
 template <int LT, int QQ>
@@ -138,16 +146,29 @@ __global__ __launch_bounds__(64 * kWaves) void balance_part_kernel(const float *
 #pragma unroll
         for (int q = 0; q < QQ; ++q) acc[q] = 0.0f;
         __syncthreads();
+        // the next step's logits are on their way while this one's are worked on
+        float next[QQ];
+        auto counted = [&](int64_t t) { return t < hi && (!mask || mask[t] != 0); };
+        bool nlive = counted(lo + slot);
+        int nid = nlive && r < k ? ids[(lo + slot) * k + r] : -1;
+        load_token<LT, QQ>(logits + (lo + slot) * E, nlive, r, E, next);
         for (int64_t tb = lo; tb < hi; tb += TPB) {
             const int64_t t = tb + slot;
-            const bool live = t < hi && (!mask || mask[t] != 0);
+            const bool live = nlive;
             float p[QQ];
-            token_softmax<LT, QQ>(logits + t * E, live, r, E, p);
+#pragma unroll
+            for (int q = 0; q < QQ; ++q) p[q] = next[q];
+            const int id = nid;
+            nlive = counted(t + TPB);
+            nid = nlive && r < k ? ids[(t + TPB) * k + r] : -1;
+            load_token<LT, QQ>(logits + (t + TPB) * E, nlive, r, E, next);
+            token_softmax<LT, QQ>(live, r, E, p);
 #pragma unroll
             for (int q = 0; q < QQ; ++q) acc[q] += p[q];
             if (live) {
                 n += r == 0 ? 1 : 0;
-                for (int j = r; j < k; j += LT) {
+                if (id >= 0 && id < E) atomicAdd(&sc[id], 1);
+                for (int j = r + LT; j < k; j += LT) {
                     const int e = ids[t * k + j];
                     if (e >= 0 && e < E) atomicAdd(&sc[e], 1);
                 }
@@ -209,6 +230,8 @@ __device__ __forceinline__ V block_sum(V v, V *red) {  // 1024 threads, fixed or
     return v;
 }
 
+// A block per sequence and 32 experts.  The rows' values are asked for first;
+// what the counts need (n_s, S') comes beside them.
 __global__ __launch_bounds__(1024) void balance_final_kernel(int64_t T, int E, int k, const int32_t *off, int S,
                                                              int chunk, float alpha, BalanceWs ws, float *loss,
                                                              int32_t *counts, float *coef) {
@@ -217,39 +240,42 @@ __global__ __launch_bounds__(1024) void balance_final_kernel(int64_t T, int E, i
     __shared__ double sp[1024];
     __shared__ int32_t sc[1024];
     __shared__ int last;
-    const int s = blockIdx.x;
+    constexpr int W = kFinalExperts, parts = 1024 / W;
+    const int eb = static_cast<int>(gridDim.x) / S;  // blocks of a sequence
+    const int s = blockIdx.x / eb;
+    const int e = (blockIdx.x % eb) * W + threadIdx.x % W, part = threadIdx.x / W;
     int64_t lo, hi;
-    // S': sequences that count a token.  A sequence's first piece mostly tells.
-    int some = 0;
-    for (int i = threadIdx.x; i < S; i += 1024) {
-        piece_rows(off, i, T, chunk, &lo, &hi);
-        int any = 0;
-        for (int64_t b = lo; b < hi && !any; ++b) any = ws.nsum[b] > 0;
-        some += any;
-    }
-    some = block_sum(some, redi);
     piece_rows(off, s, T, chunk, &lo, &hi);
-    int n = 0;
-    for (int64_t b = lo + threadIdx.x; b < hi; b += 1024) n += ws.nsum[b];
-    n = block_sum(n, redi);
-    // an expert per lane, the rest of the block shares the rows
-    const int width = E <= 64 ? 64 : E <= 128 ? 128 : E <= 256 ? 256 : E <= 512 ? 512 : 1024;
-    const int e = threadIdx.x & (width - 1), part = threadIdx.x / width, parts = 1024 / width;
     double p = 0.0;
-    int32_t c = 0;
-    if (e < E)
+    int32_t c = 0, n = 0;
+    if (e < E) {
+#pragma unroll 4
         for (int64_t b = lo + part; b < hi; b += parts) {
             p += ws.psum[b * E + e];
             c += ws.csum[b * E + e];
         }
+    }
+    for (int64_t b = lo + threadIdx.x; b < hi; b += 1024) n += ws.nsum[b];
+    // S': sequences that count a token.  A sequence's first piece mostly tells.
+    int some = 0;
+    if (S > 1) {
+        for (int i = threadIdx.x; i < S; i += 1024) {
+            int64_t a, z;
+            piece_rows(off, i, T, chunk, &a, &z);
+            int any = 0;
+            for (; a < z && !any; ++a) any = ws.nsum[a] > 0;
+            some += any;
+        }
+    }
     sp[threadIdx.x] = p;
     sc[threadIdx.x] = c;
-    __syncthreads();
+    n = block_sum(n, redi);
+    some = S > 1 ? block_sum(some, redi) : 1;
     double l = 0.0;
-    if (part == 0 && e < E) {
+    if (part == 0 && e < E) {  // row groups in order
         for (int i = 1; i < parts; ++i) {
-            p += sp[i * width + e];
-            c += sc[i * width + e];
+            p += sp[i * W + threadIdx.x];
+            c += sc[i * W + threadIdx.x];
         }
         const double nn = n;
         const double f = n > 0 ? static_cast<double>(alpha) * E * c / (k * nn * nn * some) : 0.0;
@@ -257,23 +283,26 @@ __global__ __launch_bounds__(1024) void balance_final_kernel(int64_t T, int E, i
         coef[static_cast<int64_t>(s) * E + e] = static_cast<float>(f);
         l = n > 0 ? f * p : 0.0;
     }
-    l = block_sum(l, red);
-    if (S == 1) {
+    if (threadIdx.x < 64) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor(l, o, 64);  // the 32 experts are in lanes 0 .. 31
+    }
+    if (gridDim.x == 1) {
         if (threadIdx.x == 0) *loss = static_cast<float>(l);
         return;
     }
-    // the last block to come adds the sequences' losses (the ticket was cleared
-    // by the kernel before); nobody waits for anybody
+    // the last block to come adds the blocks' losses in order (the ticket was
+    // cleared by the kernel before); nobody waits for anybody
     if (threadIdx.x == 0) {
-        __hip_atomic_store(&ws.seq_loss[s], l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(&ws.part_loss[blockIdx.x], l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         const int got = __hip_atomic_fetch_add(ws.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-        last = got == S - 1;
+        last = got == static_cast<int>(gridDim.x) - 1;
     }
     __syncthreads();
     if (!last) return;
     l = 0.0;
-    for (int i = threadIdx.x; i < S; i += 1024)
-        l += __hip_atomic_load(&ws.seq_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += 1024)
+        l += __hip_atomic_load(&ws.part_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     l = block_sum(l, red);
     if (threadIdx.x == 0) *loss = static_cast<float>(l);
 }
@@ -289,7 +318,8 @@ __global__ __launch_bounds__(64 * kWaves) void balance_bwd_kernel(const float *_
     const int s = b.seq_offsets ? find_sequence<LT>(b.seq_offsets, b.S, t) : 0;
     const bool live = t < T && s >= 0 && s < b.S && (!b.mask || b.mask[t] != 0);
     float p[QQ], g[QQ];
-    token_softmax<LT, QQ>(logits + t * E, live, r, E, p);
+    load_token<LT, QQ>(logits + t * E, live, r, E, p);
+    token_softmax<LT, QQ>(live, r, E, p);
     const float *co = b.coef + static_cast<int64_t>(live ? s : 0) * E;
     const float up = b.dloss ? *b.dloss : 1.0f;
     float c = 0.0f;
@@ -346,7 +376,7 @@ hipError_t launch_balance_loss(const float *logits, const int32_t *ids, int64_t 
 #undef XMOE_BALANCE_PART
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(balance_final_kernel, dim3(static_cast<unsigned>(S)), dim3(1024), 0, st, T, E, k, seq_offsets,
+    hipLaunchKernelGGL(balance_final_kernel, dim3(static_cast<unsigned>(S * final_blocks(E))), dim3(1024), 0, st, T, E, k, seq_offsets,
                        S, chunk, alpha, w, loss, counts, coef);
     return hipGetLastError();
 }

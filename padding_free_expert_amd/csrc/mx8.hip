@@ -158,125 +158,184 @@ struct Mx8Args {
     bf16_t *y;                  // down: ye [rows, N]
 };
 
-__device__ __forceinline__ i32x8_t frag8(uint4 lo, uint4 hi) {
-    return i32x8_t{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
-                   static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
+// The tile of this block for launches whose blocks take one tile each: every
+// wave finds it by itself from the offsets, lane l counting the row tiles of
+// groups per * l .. + per - 1.  Tiles as in resolve_tile; false: no tile.
+template <int BM>
+__device__ __forceinline__ bool wave_tile(const GemmArgs &p, int v, int tiles_n, Tile *t) {
+    const int lane = threadIdx.x & 63;
+    const int per = (p.G + 63) / 64, g0 = lane * per;
+    const int mt = v / tiles_n;
+    int64_t lo = 0, hi = 0;
+    int cnt = 0;
+    for (int i = 0; i < per; ++i) {
+        if (g0 + i < p.G) {
+            seg_bounds(p, g0 + i, &lo, &hi);
+            cnt += static_cast<int>((hi - lo + BM - 1) / BM);
+        }
+    }
+    int inc = cnt;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int u = __shfl_up(inc, off, 64);
+        if (lane >= off) inc += u;
+    }
+    const unsigned long long past = __ballot(inc <= mt);
+    if (past == ~0ull) return false;
+    const int owner = __popcll(past);  // the first lane whose groups reach the tile
+    int first = __shfl(inc - cnt, owner, 64), g = owner * per, n;
+    for (int i = 0; ; ++i) {
+        if (per > 1) seg_bounds(p, g + i, &lo, &hi);
+        else lo = __shfl(static_cast<int>(lo), owner, 64), hi = __shfl(static_cast<int>(hi), owner, 64);
+        n = static_cast<int>((hi - lo + BM - 1) / BM);
+        if (mt < first + n) {
+            g += i;
+            break;
+        }
+        first += n;
+    }
+    const int local = v - first * tiles_n;
+    t->g = __builtin_amdgcn_readfirstlane(g);
+    t->m0 = __builtin_amdgcn_readfirstlane((local % n) * BM);
+    t->nt = __builtin_amdgcn_readfirstlane(local / n);
+    const int base = __builtin_amdgcn_readfirstlane(static_cast<int>(lo));
+    t->base = base;
+    t->Mg = __builtin_amdgcn_readfirstlane(static_cast<int>(hi)) - base;
+    t->Kg = 0;
+    return true;
 }
 
 // Few rows per expert: the weights are streamed past the rows once.  A block
-// takes 16 MT rows by 32 columns of one expert (of W1 and of W3 for the
-// up-projection, NB = 2) and its KW waves split the summed axis in 128-deep
-// steps; operands go from memory straight to registers, since no other wave of
-// the block needs them.  The waves' partial sums meet in LDS, added in wave
-// order.
+// takes 16 MT rows of one expert by 64 weight rows (32 of W1 and the same of W3
+// for the up-projection, NB = 2) and its four waves split the summed axis in
+// 128-deep steps; operands go from memory straight to registers, since no other
+// wave of the block needs them.  The waves' partial sums meet in LDS, added in
+// wave order.  Bound by the weights' bytes: what counts is loads in flight, so
+// registers are kept few enough for five blocks on a compute unit rather than
+// spent on a second step's loads (that form was 1.6 times slower).
 template <int NB, int MT, int KW>
-__global__ __launch_bounds__(64 * KW) void mx8_stream_kernel(Mx8Args p) {
-    constexpr int BM = 16 * MT, BN = 32;
-    constexpr int NF = NB * 2 * MT;  // 16 x 16 results of a wave
+__global__ __launch_bounds__(64 * KW) void mx8_stream_kernel(
+    Mx8Args p) {
+    constexpr int NC = 4 / NB, BM = 16 * MT, BN = 16 * NC;
+    constexpr int NF = 4 * MT;  // 16 x 16 results of a wave
     __shared__ f32x4_t part[KW][NF][64];
-    static_assert(sizeof(part) <= 64 * 1024, "partial sums");
-    static_assert(KW >= MT, "one wave for each 16 rows of the result");
-    Tile t;
-    if (!resolve_tile<BM, BN>(p.g, &t, blockIdx.x, gridDim.x)) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int l16 = lane & 15, quad = lane >> 4;
+    static_assert(sizeof(part) <= 32 * 1024, "five blocks on a compute unit");
+    static_assert(KW >= MT * (NB == 1 ? 2 : 1), "a wave for each 16 rows (and 32 columns) of the result");
     const int N = p.g.N, K = p.K, kb = (K + 127) / 128;
+    Tile t;
+    if (!wave_tile<BM>(p.g, xcd_tile_order(blockIdx.x, gridDim.x), (N + BN - 1) / BN, &t)) return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, quad = lane >> 4;
     const int n0 = t.nt * BN;
 
-    // this lane's rows of both operands
-    const uint8_t *ap[MT], *asp[MT];
-    bool arow[MT];
+    // offsets of this lane's rows from uniform bases that move with k
+    const uint8_t *wb[2], *ws[2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        wb[b] = (b ? p.b1 : p.b0) + (static_cast<int64_t>(t.g) * N + n0) * K;
+        ws[b] = (b ? p.b1s : p.b0s) + (static_cast<int64_t>(t.g) * kb * N + n0) * 4;
+    }
+    uint32_t boff[NC], bsoff[NC], aoff[MT], asoff[MT];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        const int n = min(16 * j + l16, N - 1 - n0);  // past N: a row again, not stored
+        boff[j] = static_cast<uint32_t>(n) * static_cast<uint32_t>(K) + 16 * quad;
+        bsoff[j] = 4u * n;
+    }
+    // rows past the group's end read its first row and are not stored; ids outside
+    // the rows read row 0 and count as zeros
+    const uint8_t *const ab = p.map ? p.a : p.a + (t.base + t.m0) * K;
+    const uint8_t *const as = p.map ? p.as : p.as + (t.base + t.m0) * 4;
+    bool zero[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const int m = t.m0 + 16 * i + l16;
-        arow[i] = m < t.Mg;
-        int64_t r = arow[i] ? t.base + m : 0;
-        if (arow[i] && p.map) {
-            r = p.map[r];
-            if (r < 0 || r >= p.a_rows) {  // outside the rows: a row of zeros
-                arow[i] = false;
-                r = 0;
-            }
-        }
-        ap[i] = p.a + r * K + 16 * quad;
-        asp[i] = p.as + r * 4;
+        const int m = t.m0 + 16 * i + l16 < t.Mg ? 16 * i + l16 : 0;
+        int id = p.map ? p.map[t.base + t.m0 + m] : m;
+        zero[i] = p.map && (id < 0 || id >= p.a_rows);
+        if (zero[i]) id = 0;
+        aoff[i] = static_cast<uint32_t>(id) * static_cast<uint32_t>(K) + 16 * quad;
+        asoff[i] = 4u * id;
     }
-    const uint8_t *bp[NB][2], *bsp[NB][2];
+    f32x4_t acc[NB][NC][MT];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int n = n0 + 16 * j + l16;
-            bp[b][j] = (b ? p.b1 : p.b0) + (static_cast<int64_t>(t.g) * N + n) * K + 16 * quad;
-            bsp[b][j] = (b ? p.b1s : p.b0s) + (static_cast<int64_t>(t.g) * kb * N + n) * 4;
-        }
-    f32x4_t acc[NB][2][MT];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NC; ++j)
 #pragma unroll
             for (int i = 0; i < MT; ++i) acc[b][j][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    auto load = [&](const uint8_t *q, int64_t k, bool lo, bool hi) {
-        return frag8(lo ? *reinterpret_cast<const uint4 *>(q + k) : zero,
-                     hi ? *reinterpret_cast<const uint4 *>(q + k + 64) : zero);
+    struct Step {
+        i32x8_t b[NB][NC], a[MT];
+        int bs[NB][NC], as[MT];
     };
-    // one 128-deep step; TAIL: K ends inside it (elements past K are zeros)
-    auto step = [&](int s, auto tail) {
-        constexpr bool TAIL = decltype(tail)::value;
+    auto fetch = [&](int s, Step &f) {
         const int64_t k = static_cast<int64_t>(s) * 128;
-        const bool lo = !TAIL || k + 16 * quad < K, hi = !TAIL || k + 64 + 16 * quad < K;
-        i32x8_t fb[NB][2], fa[MT];
-        int sb[NB][2], sa[MT];
+        const bool whole = k + 128 <= K;  // else K ends inside: elements past it are zeros
+        const bool lo = whole || k + 16 * quad < K, hi = whole || k + 64 + 16 * quad < K;
+        auto load = [&](const uint8_t *q, uint32_t off) {
+            const i32x4_t z = {0, 0, 0, 0};
+            const auto *a = reinterpret_cast<const i32x4_t *>(q + off);
+            const i32x4_t x = lo ? __builtin_nontemporal_load(a) : z, y = hi ? __builtin_nontemporal_load(a + 4) : z;
+            return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+        };
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                fb[b][j] = load(bp[b][j], k, lo, hi);
-                sb[b][j] = *reinterpret_cast<const int *>(bsp[b][j] + static_cast<int64_t>(s) * N * 4);
+            for (int j = 0; j < NC; ++j) {
+                f.b[b][j] = load(wb[b] + k, boff[j]);
+                f.bs[b][j] = *reinterpret_cast<const int *>(ws[b] + static_cast<int64_t>(s) * N * 4 + bsoff[j]);
             }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            fa[i] = load(ap[i], k, lo && arow[i], hi && arow[i]);
-            sa[i] = *reinterpret_cast<const int *>(asp[i] + static_cast<int64_t>(s) * p.a_rows * 4);
-            if (!arow[i]) sa[i] = 0x7f7f7f7f;
+            f.a[i] = load(ab + k, aoff[i]);
+            f.as[i] = *reinterpret_cast<const int *>(as + static_cast<int64_t>(s) * p.a_rows * 4 + asoff[i]);
         }
+    };
+    auto multiply = [&](const Step &f) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NC; ++j)
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
                     acc[b][j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        fb[b][j], fa[i], acc[b][j][i], 0, 0, 0, sb[b][j] >> (8 * quad), 0, sa[i] >> (8 * quad));
+                        f.b[b][j], f.a[i], acc[b][j][i], 0, 0, 0, f.bs[b][j] >> (8 * quad), 0, f.as[i] >> (8 * quad));
     };
-    const int full = K / 128;
-    for (int s = wave; s < full; s += KW) step(s, std::false_type{});
-    if (full < kb && full % KW == wave) step(full, std::true_type{});
-
+#pragma unroll 1
+    for (int s = wave; s < kb; s += KW) {
+        Step f;
+        fetch(s, f);
+        multiply(f);
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NC; ++j)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) part[wave][(b * 2 + j) * MT + i][lane] = acc[b][j][i];
+            for (int i = 0; i < MT; ++i) part[wave][(b * NC + j) * MT + i][lane] = acc[b][j][i];
     __syncthreads();
-    if (wave >= MT) return;
-    // wave i: rows 16 i .. 16 i + 15; lane l has row l % 16, columns 16 j + 4 (l / 16) + r
-    const int m = t.m0 + 16 * wave + l16;
+    // wave i (and, for the down-projection, MT + i for the upper 32 columns): rows
+    // 16 i .. 16 i + 15; lane l has row l % 16, columns 16 j + 4 (l / 16) + r
+    if (wave >= MT * (NB == 1 ? 2 : 1)) return;
+    const int mi = wave % MT, j0 = 2 * (wave / MT);
+    const int c0 = n0 + 16 * j0;
+    const int m = t.m0 + 16 * mi + l16;
     const int64_t row = t.base + m;
-    const bool live = m < t.Mg;
+    const bool live = m < t.Mg && c0 < N;
+    bool none = false;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) none = i == mi ? zero[i] : none;
     f32x4_t v[NB][2];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int f = (b * 2 + j) * MT + wave;
+            const int f = (b * NC + j0 + j) * MT + mi;
             v[b][j] = part[0][f][lane];
 #pragma unroll
             for (int w = 1; w < KW; ++w) v[b][j] += part[w][f][lane];
+            if (none) v[b][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         }
     if constexpr (NB == 2) {
         float o[8];
@@ -293,26 +352,23 @@ __global__ __launch_bounds__(64 * KW) void mx8_stream_kernel(Mx8Args p) {
         if (live) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                *reinterpret_cast<uint32_t *>(p.q + row * N + n0 + 16 * j + 4 * quad) =
+                *reinterpret_cast<uint32_t *>(p.q + row * N + c0 + 16 * j + 4 * quad) =
                     mx8_pack4(o[4 * j] * sc, o[4 * j + 1] * sc, o[4 * j + 2] * sc, o[4 * j + 3] * sc);
             // the scale byte of this block of 32 columns; the last block also fills its group
-            const int blk = n0 / 32;
+            const int blk = c0 / 32;
             const int at = (blk & 3) + quad;
-            if (quad == 0 || (n0 + 32 >= N && at < 4))
+            if (quad == 0 || (c0 + 32 >= N && at < 4))
                 p.qs[(static_cast<int64_t>(blk >> 2) * p.g.extent + row) * 4 + at] =
                     static_cast<uint8_t>(quad == 0 ? byte : kMxOne);
         }
     } else if (live) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            *reinterpret_cast<uint2 *>(p.y + row * N + n0 + 16 * j + 4 * quad) =
-                make_uint2(pack_bf16x2(v[0][j][0], v[0][j][1]), pack_bf16x2(v[0][j][2], v[0][j][3]));
+            *reinterpret_cast<uint2 *>(p.y + row * N + c0 + 16 * j + 4 * quad) =
+                make_uint2(cvt_bf16x2(v[0][j][0], v[0][j][1]), cvt_bf16x2(v[0][j][2], v[0][j][3]));
     }
 }
 
-// The tiles of a launch, found from the device-side offsets once per block and
-// kept in shared memory: for each expert its rows and the number of row tiles
-// up to and including its own.
 // A value that the compiler takes as new at this point: what follows from it is
 // computed here instead of being kept in registers across the loop around it.
 __device__ __forceinline__ uint32_t fresh(uint32_t v) {
@@ -731,14 +787,14 @@ hipError_t launch_tile(const Mx8Args &p, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int NB, int MT, int KW>
+template <int NB, int MT>
 hipError_t launch_stream(const Mx8Args &p, hipStream_t s) {
     // no expert without rows has a tile: at most rows / BM whole ones and one
     // more for each expert that has rows
     const int64_t tiles = p.g.extent / (16 * MT) + std::min<int64_t>(p.g.G, p.g.extent);
-    const int64_t grid = tiles * (p.g.N / 32);
+    const int64_t grid = tiles * ((p.g.N + 64 / NB - 1) / (64 / NB));
     if (grid <= 0) return hipSuccess;
-    hipLaunchKernelGGL((mx8_stream_kernel<NB, MT, KW>), dim3(static_cast<unsigned>(grid)), dim3(64 * KW), 0, s, p);
+    hipLaunchKernelGGL((mx8_stream_kernel<NB, MT>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
@@ -757,8 +813,16 @@ Mx8Args rows_args(const int32_t *offsets, int E, int64_t rows, int N, int K) {
 
 template <int NB>
 hipError_t product(const Mx8Args &p, hipStream_t s) {
-    // few rows per expert: the weights' bytes bound it
-    if (p.g.extent <= 48 * static_cast<int64_t>(p.g.G)) return launch_stream<NB, 2, 8>(p, s);
+    // Up to 10 rows per expert the stream kernel reads the weights faster (9 rows
+    // on 64 experts of d = 2048, h = 1408, up and down: 86 + 45 us against the tile
+    // kernel's 98 + 46; 12 rows: 100 + 51 against 98 + 46).  Where the tile kernel
+    // has no tile for every compute unit, the stream kernel's 32-row form, whose
+    // tiles are 64 columns narrow, is ahead up to 64 rows (4 experts of 64 rows: 29
+    // + 17 against 37 + 21 us; of 128 rows: 41 + 22 against 37 + 21).
+    const int64_t rows = p.g.extent, active = std::min<int64_t>(p.g.G, rows);
+    const int64_t tiles = (rows / 256 + active) * ((p.g.N + 256 / NB - 1) / (256 / NB));
+    if (rows <= 10 * active) return launch_stream<NB, 1>(p, s);
+    if (tiles < kComputeUnits && rows <= 64 * active) return launch_stream<NB, 2>(p, s);
     if constexpr (NB == 2) {
         if (p.map) return launch_tile<2, true>(p, s);
     }

@@ -208,23 +208,26 @@ __global__ __launch_bounds__(64 * NW) void add_rmsnorm_bwd_kernel(const T *dy, c
     }
 }
 
-// dgamma[c] = sum over the blocks' partial sums: 64 columns a block, its 16
-// waves take every 16th partial and meet in LDS (fixed order).
+// dgamma[c] = sum over the blocks' partial sums: 32 columns a block, whose 32 row
+// groups take every 32nd partial and meet in LDS (fixed order).
 __global__ __launch_bounds__(1024) void dgamma_kernel(const float *__restrict__ part, int nblk, int d,
                                                       float *__restrict__ dgamma) {
-    __shared__ float s[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
+    __shared__ float s[32][33];
+    const int col = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + col;
     float v = 0.0f;
-    if (c < d)
-        for (int b = wave; b < nblk; b += 16) v += part[static_cast<int64_t>(b) * d + c];
-    s[wave][lane] = v;
-    __syncthreads();
-    if (wave == 0 && c < d) {
-#pragma unroll
-        for (int w = 1; w < 16; ++w) v += s[w][lane];
-        dgamma[c] = v;
+    if (c < d) {
+#pragma unroll 8
+        for (int b = grp; b < nblk; b += 32) v += part[static_cast<int64_t>(b) * d + c];
     }
+    s[grp][col] = v;
+    __syncthreads();
+    // a wave per two columns' 32 sums
+    v = s[threadIdx.x & 31][threadIdx.x >> 5];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    const int w = blockIdx.x * 32 + (threadIdx.x >> 5);
+    if ((threadIdx.x & 31) == 0 && w < d) dgamma[w] = v;
 }
 
 // Waves per row and vectors per lane: a row of nvec 16-byte vectors.  Up to 4
@@ -335,7 +338,7 @@ hipError_t launch_add_rmsnorm_bwd(int dt, const void *dy, const void *dsum, cons
         if (e != hipSuccess) return e;
     }
     // no rows: dgamma = 0
-    hipLaunchKernelGGL(dgamma_kernel, dim3(static_cast<unsigned>((d + 63) / 64)), dim3(1024), 0, s, part, n, d, dgamma);
+    hipLaunchKernelGGL(dgamma_kernel, dim3(static_cast<unsigned>((d + 31) / 32)), dim3(1024), 0, s, part, n, d, dgamma);
     return hipGetLastError();
 }
 

@@ -181,6 +181,15 @@ def test_binding_checks_its_tensors(xm):
 
 
 def test_tensors_of_two_devices_are_refused(xm):
-    a, b = torch.zeros(2, 32, dtype=BF), torch.zeros(2, 32, dtype=F8, device="meta")
+    class On:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def get_device(self):
+            return self.dev
     with pytest.raises(ValueError, match="different devices"):
-        xm.xmoe_mx8_quantize(a, b, torch.zeros(1, 2, 4, dtype=U8))
+        xm._on_device(On(0), None, On(1))
+    with pytest.raises(ValueError, match="different devices"):
+        xm._on_device(On(0), On(-1))
+    with xm._on_device(On(-1), None, On(-1)):   # host tensors: refused when their pointers are taken
+        pass
