@@ -213,10 +213,9 @@ __device__ __forceinline__ bool wave_tile(const GemmArgs &p, int v, int tiles_n,
 // wave order.  Bound by the weights' bytes: what counts is loads in flight, so
 // registers are kept few enough for five blocks on a compute unit rather than
 // spent on a second step's loads (that form was 1.6 times slower).
-template <int NB, int MT, int KW>
-__global__ __launch_bounds__(64 * KW) void mx8_stream_kernel(
-    Mx8Args p) {
-    constexpr int NC = 4 / NB, BM = 16 * MT, BN = 16 * NC;
+template <int NB, int MT>
+__global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
+    constexpr int KW = 4, NC = 4 / NB, BM = 16 * MT, BN = 16 * NC;
     constexpr int NF = 4 * MT;  // 16 x 16 results of a wave
     __shared__ f32x4_t part[KW][NF][64];
     static_assert(sizeof(part) <= 32 * 1024, "five blocks on a compute unit");
