@@ -12,10 +12,13 @@ from typing import Dict
 
 import torch
 
-from . import (PFT, xmoe_build_pft, xmoe_build_pft_shared, xmoe_build_pft_workspace_size, xmoe_combine,
+from . import (PFT, mx8_scale_shape, xmoe_add_rmsnorm, xmoe_add_rmsnorm_bwd, xmoe_add_rmsnorm_bwd_workspace_size,
+               xmoe_balance_loss, xmoe_balance_loss_workspace_size, xmoe_build_pft, xmoe_build_pft_shared,
+               xmoe_build_pft_workspace_size, xmoe_combine,
                xmoe_combine_bwd, xmoe_dispatch_bwd, xmoe_expert_ffn_bwd,
                xmoe_expert_ffn_bwd_dact_gather, xmoe_expert_ffn_bwd_dw13_gather, xmoe_expert_ffn_bwd_dw2, xmoe_expert_ffn_bwd_dx,
-               xmoe_expert_ffn_down, xmoe_expert_ffn_up, xmoe_expert_ffn_up_gather, xmoe_route, xmoe_route_bwd,
+               xmoe_expert_ffn_down, xmoe_expert_ffn_down_mx8, xmoe_expert_ffn_up, xmoe_expert_ffn_up_gather,
+               xmoe_expert_ffn_up_mx8, xmoe_mx8_quantize_weights, xmoe_route, xmoe_route_bwd, xmoe_route_bwd_balance,
                xmoe_route_bwd_workspace_size, xmoe_route_workspace_size)
 
 
@@ -45,10 +48,17 @@ class PaddingFreeMoE:
     on the DeepSeek-MoE-16B shape the separate stream is ~2.7% faster: it fills
     the routed products' tails, and the merged buffer's mean rows per expert
     (routed and shared together) moves the down-projection and dA products to
-    the smaller tile."""
+    the smaller tile.
+
+    balance_alpha > 0 adds the gate's balance loss: the forward leaves it in
+    `loss` [1] and the per-expert slot counts in `counts` [n_seq, E] (its kernels
+    run beside the experts), and the backward adds its gradient, times `dloss`,
+    to the gate's.  n_seq sequences, whose tokens the forward's seq_offsets
+    names (n_seq = 1: all tokens, or those it names)."""
 
     def __init__(self, weights: Dict[str, torch.Tensor], T: int, k: int, inv_tau: float = 1.0,
-                 backward: bool = True, lean: bool = False, overlap: bool = True, merge_shared: bool = False):
+                 backward: bool = True, lean: bool = False, overlap: bool = True, merge_shared: bool = False,
+                 balance_alpha: float = 0.0, n_seq: int = 1):
         self.w = weights
         wg, w1 = weights["wg"], weights["w1"]
         self.dtype = wg.dtype
@@ -93,6 +103,12 @@ class PaddingFreeMoE:
         self.pft = PFT(T, Ec, kc, dev)
         self.pft_ws = torch.empty(max(xmoe_build_pft_workspace_size(T, Ec, kc), 16), dtype=torch.uint8, device=dev)
         self.route_ws = torch.empty(max(xmoe_route_workspace_size(T, d, E, dt), 16), dtype=torch.uint8, device=dev)
+        self.balance_alpha, self.n_seq = balance_alpha, n_seq
+        if balance_alpha > 0:
+            self.loss = torch.empty(1, **f32)
+            self.counts = torch.empty((n_seq, E), dtype=torch.int32, device=dev)
+            self.coef = torch.empty((n_seq, E), **f32)
+            self.balance_ws = torch.empty(xmoe_balance_loss_workspace_size(T, E, n_seq), dtype=torch.uint8, device=dev)
         self.act = torch.empty((R, h), dtype=dt, device=dev)
         self.h13 = torch.empty((R, 2 * h), dtype=dt, device=dev) if backward else None
         self.ye = torch.empty((R, d), dtype=dt, device=dev)
@@ -156,8 +172,12 @@ class PaddingFreeMoE:
         side = self.side if (self.side_shared and self.overlap) else main
         return main, side
 
-    def forward(self, x: torch.Tensor, stream=None, hook=None, probe=None) -> torch.Tensor:
-        """hook(name), if given, is called after each library call is enqueued.
+    def forward(self, x: torch.Tensor, stream=None, hook=None, probe=None, seq_offsets=None,
+                token_mask=None) -> torch.Tensor:
+        """seq_offsets int32 [n_seq + 1] and token_mask bool [T]: the tokens that the
+        balance loss counts (None: one sequence, every token).  The backward
+        reads them again.
+        hook(name), if given, is called after each library call is enqueued.
         probe(name, stream), if given, is called right before and right after
         each up-projection launch ("up" / "up_end" for the routed experts,
         "shared_up" / "shared_up_end" for the shared ones) with the stream the
@@ -179,6 +199,18 @@ class PaddingFreeMoE:
         xmoe_route(x, w["wg"], self.k, self.topk_ids, self.topk_w, self.logits, self.inv_tau,
                    w.get("logit_bias"), w.get("select_bias"), workspace=self.route_ws, stream=main)
         mark("route")
+        bs = main
+        if self.balance_alpha > 0:
+            if self.n_seq > 1 and seq_offsets is None:
+                raise ValueError("seq_offsets is required for more than one sequence")
+            self.seq_offsets, self.token_mask = seq_offsets, token_mask
+            if self.overlap and self.gside is not None:
+                bs = self.gside
+                bs.wait_stream(main)
+            xmoe_balance_loss(self.logits, self.topk_ids, self.balance_alpha, self.loss, self.counts, self.coef,
+                              seq_offsets, token_mask, self.balance_ws, stream=bs)
+            if bs is main:
+                mark("balance_loss")
         if self.merged:
             xmoe_build_pft_shared(self.topk_ids, self.topk_w, self.E, self.ns, self.pft, self.pft_ws, stream=main)
         else:
@@ -196,10 +228,14 @@ class PaddingFreeMoE:
             y_add = self.sh_y
         xmoe_combine(self.ye, self.pft, self.T, self.y, y_add=y_add, stream=main)
         mark("combine")
+        if bs is not main:
+            main.wait_stream(bs)
         self.x = x
         return self.y
 
-    def backward(self, dy: torch.Tensor, stream=None, hook=None) -> torch.Tensor:
+    def backward(self, dy: torch.Tensor, stream=None, hook=None, dloss=None) -> torch.Tensor:
+        """dloss: upstream gradient of the balance loss, fp32 [1] on the device
+        (None: 1)."""
         w = self.w
         mark = hook or (lambda name: None)
         main, side = self._streams(stream)
@@ -236,8 +272,13 @@ class PaddingFreeMoE:
             gs = side
         if gs is not ws:
             gs.wait_stream(ws)
-        xmoe_route_bwd(self.x, w["wg"], self.logits, self.topk_ids, self.dtopk_w, rdst, self.dwg,
-                       self.rbwd_ws, self.inv_tau, accumulate=self.side_shared, stream=gs)
+        if self.balance_alpha > 0:
+            xmoe_route_bwd_balance(self.x, w["wg"], self.logits, self.topk_ids, self.dtopk_w, self.coef, rdst, self.dwg,
+                                   self.rbwd_ws, self.inv_tau, accumulate=self.side_shared,
+                                   seq_offsets=self.seq_offsets, token_mask=self.token_mask, dloss=dloss, stream=gs)
+        else:
+            xmoe_route_bwd(self.x, w["wg"], self.logits, self.topk_ids, self.dtopk_w, rdst, self.dwg,
+                           self.rbwd_ws, self.inv_tau, accumulate=self.side_shared, stream=gs)
         if gs is main:
             mark("route_bwd")
         dx_add = rdst
@@ -331,3 +372,114 @@ class PaddingFreeMoE:
         if self.shared:
             g.update(ds1=self.ds1[0], ds3=self.ds3[0], ds2=self.ds2[0])
         return g
+
+
+class MoEBlock:
+    """Pre-norm and layer of a transformer block, for training:
+      sum = x + residual;  y = rmsnorm(sum) * gamma;  out = layer(y)
+    The caller's next block adds out to sum.  weights: the layer's, with "norm"
+    (gamma [d]); the other arguments are PaddingFreeMoE's."""
+
+    def __init__(self, weights: Dict[str, torch.Tensor], T: int, k: int, eps: float = 1e-6, **layer):
+        self.moe = PaddingFreeMoE(weights, T, k, **layer)
+        self.gamma, self.eps = weights["norm"], eps
+        m = self.moe
+        row = dict(dtype=m.dtype, device=m.device)
+        self.sum = torch.empty((T, m.d), **row)
+        self.y = torch.empty((T, m.d), **row)
+        self.rstd = torch.empty(T, dtype=torch.float32, device=m.device)
+        if m.backward_enabled:
+            self.dx = torch.empty((T, m.d), **row)
+            self.dgamma = torch.empty(m.d, dtype=torch.float32, device=m.device)
+            self.ws = torch.empty(xmoe_add_rmsnorm_bwd_workspace_size(T, m.d, m.dtype), dtype=torch.uint8,
+                                  device=m.device)
+
+    def forward(self, x: torch.Tensor, residual=None, stream=None, **tokens):
+        """(out, sum); tokens: the layer's seq_offsets and token_mask."""
+        xmoe_add_rmsnorm(x, residual, self.gamma, self.eps, self.sum, self.y, rstd=self.rstd, stream=stream)
+        return self.moe.forward(self.y, stream=stream, **tokens), self.sum
+
+    def backward(self, dout: torch.Tensor, dsum=None, stream=None, dloss=None) -> torch.Tensor:
+        """Gradient of x (and of residual) from those of out and sum; gamma's is in
+        `dgamma`, the layer's where the layer leaves them."""
+        dy = self.moe.backward(dout, stream=stream, dloss=dloss)
+        xmoe_add_rmsnorm_bwd(dy, dsum, self.sum, self.gamma, self.rstd, self.dx, self.dgamma, self.ws, stream=stream)
+        return self.dx
+
+
+class MoEBlock8:
+    """The same block for serving, its experts in 8 bits: the norm leaves y for the
+    gate and y in 8 bits for the experts, whose weights are quantized once at
+    construction (again by refresh_weights() after they change).  bf16 weights
+    as PaddingFreeMoE takes them, with "norm"; d, h and the shared width
+    multiples of 32.  Shared experts run on a second stream beside the routed
+    ones.  Holds the buffers of T tokens."""
+
+    def __init__(self, weights: Dict[str, torch.Tensor], T: int, k: int, inv_tau: float = 1.0, eps: float = 1e-6,
+                 overlap: bool = True):
+        self.w, self.T, self.k, self.inv_tau, self.eps, self.overlap = weights, T, k, inv_tau, eps, overlap
+        wg, w1 = weights["wg"], weights["w1"]
+        dev, dt = wg.device, wg.dtype
+        self.device, (self.d, self.E), self.h = dev, wg.shape, w1.shape[2]
+        d, E, h, R = self.d, self.E, self.h, T * k
+        self.shared = weights.get("s1") is not None
+        f8, u8 = dict(dtype=torch.float8_e4m3fn, device=dev), dict(dtype=torch.uint8, device=dev)
+        bf = dict(dtype=torch.bfloat16, device=dev)
+
+        def rows(n, K):
+            return torch.empty((n, K), **f8), torch.empty(mx8_scale_shape(n, K), **u8)
+
+        def experts(n, N, K):
+            return torch.empty((n, N, K), **f8), torch.empty((n,) + mx8_scale_shape(N, K), **u8)
+
+        self.sum, self.y, self.out = (torch.empty((T, d), **bf) for _ in range(3))
+        self.yq, self.yqs = rows(T, d)
+        self.topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        self.topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        self.logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        self.pft = PFT(T, E, k, dev)
+        self.pft_ws = torch.empty(max(xmoe_build_pft_workspace_size(T, E, k), 16), **u8)
+        self.route_ws = torch.empty(max(xmoe_route_workspace_size(T, d, E, dt), 16), **u8)
+        self.act, self.acts = rows(R, h)
+        self.ye = torch.empty((R, d), **bf)
+        self.w1q, self.w3q, self.w2q = experts(E, h, d), experts(E, h, d), experts(E, d, h)
+        if self.shared:
+            hs = weights["s1"].shape[1]
+            self.s1q, self.s3q, self.s2q = experts(1, hs, d), experts(1, hs, d), experts(1, d, hs)
+            self.sh_off = torch.tensor([0, T], dtype=torch.int32, device=dev)
+            self.sh_act, self.sh_acts = rows(T, hs)
+            self.sh_y = torch.empty((T, d), **bf)
+            self.side = torch.cuda.Stream(device=dev)
+        self.refresh_weights()
+
+    def refresh_weights(self, stream=None) -> None:
+        """Quantize the weights (the tensors in the weights dict) again."""
+        w = self.w
+        pairs = [(w["w1"], self.w1q), (w["w3"], self.w3q), (w["w2"], self.w2q)]
+        if self.shared:
+            pairs += [(w[n].unsqueeze(0), q) for n, q in (("s1", self.s1q), ("s3", self.s3q), ("s2", self.s2q))]
+        for t, (q, s) in pairs:
+            xmoe_mx8_quantize_weights(t, q, s, stream=stream)
+
+    def forward(self, x: torch.Tensor, residual=None, stream=None):
+        """(out, sum)."""
+        w = self.w
+        main = stream if stream is not None else torch.cuda.current_stream(self.device)
+        side = self.side if self.shared and self.overlap else main
+        xmoe_add_rmsnorm(x, residual, w["norm"], self.eps, self.sum, self.y, self.yq, self.yqs, stream=main)
+        if self.shared:
+            if side is not main:
+                side.wait_stream(main)
+            xmoe_expert_ffn_up_mx8(self.yq, self.yqs, *self.s1q, *self.s3q, self.sh_off, self.sh_act, self.sh_acts,
+                                   stream=side)
+            xmoe_expert_ffn_down_mx8(self.sh_act, self.sh_acts, *self.s2q, self.sh_off, self.sh_y, stream=side)
+        xmoe_route(self.y, w["wg"], self.k, self.topk_ids, self.topk_w, self.logits, self.inv_tau, w.get("logit_bias"),
+                   w.get("select_bias"), workspace=self.route_ws, stream=main)
+        xmoe_build_pft(self.topk_ids, self.topk_w, self.E, self.pft, self.pft_ws, stream=main)
+        xmoe_expert_ffn_up_mx8(self.yq, self.yqs, *self.w1q, *self.w3q, self.pft.expert_offsets, self.act, self.acts,
+                               token_ids=self.pft.token_ids, stream=main)
+        xmoe_expert_ffn_down_mx8(self.act, self.acts, *self.w2q, self.pft.expert_offsets, self.ye, stream=main)
+        if side is not main:
+            main.wait_stream(side)
+        xmoe_combine(self.ye, self.pft, self.T, self.out, y_add=self.sh_y if self.shared else None, stream=main)
+        return self.out, self.sum
