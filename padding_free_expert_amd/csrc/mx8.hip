@@ -390,8 +390,9 @@ __device__ __forceinline__ void lds_dma4(__amdgpu_buffer_rsrc_t rs, uint32_t vof
 }
 
 struct TileTable {
-    int end[1024];  // INT_MAX past the last expert
-    int lo[1024], hi[1024];
+    int end[1024];        // row tiles up to and including the expert's; INT_MAX past the last expert
+    int lo[1024];         // first row
+    uint16_t last[1024];  // rows of its last tile
     int wave_sum[4];
 };
 
@@ -405,9 +406,10 @@ __device__ __forceinline__ int build_table(const GemmArgs &p, TileTable &tt) {
         const int g = 4 * threadIdx.x + i;
         int64_t lo = 0, hi = 0;
         if (g < p.G) seg_bounds(p, g, &lo, &hi);
+        const int n = static_cast<int>((hi - lo + BM - 1) / BM);
         tt.lo[g] = static_cast<int>(lo);
-        tt.hi[g] = static_cast<int>(hi);
-        sum += static_cast<int>((hi - lo + BM - 1) / BM);
+        tt.last[g] = static_cast<uint16_t>(n > 0 ? hi - lo - static_cast<int64_t>(n - 1) * BM : 0);
+        sum += n;
         cnt[i] = sum;
     }
     int inc = sum;
@@ -433,24 +435,30 @@ __device__ __forceinline__ int build_table(const GemmArgs &p, TileTable &tt) {
     return total;
 }
 
+// A tile of the tile kernel: rows [row, row + rows) of the experts' rows, all of
+// expert g, and columns from n0.
+struct TileAt {
+    int g, n0, rows;
+    int64_t row;
+};
+
 // Tile number v of the launch in the order of resolve_tile: an expert's tiles
 // together, its row tiles fastest.  Every wave searches by itself (64 lanes over
 // 16 entries each, then over those 16).
-__device__ __forceinline__ Tile find_tile(const TileTable &tt, int v, int tiles_n, int bm) {
+template <int BM, int BN>
+__device__ __forceinline__ TileAt find_tile(const TileTable &tt, int v, int tiles_n) {
     const int lane = threadIdx.x & 63;
     const int mt = v / tiles_n;
     const int blk = __popcll(__ballot(tt.end[16 * lane + 15] <= mt));
-    const int g = 16 * blk + __popcll(__ballot(lane < 16 && tt.end[16 * blk + (lane & 15)] <= mt));
+    const int g = __builtin_amdgcn_readfirstlane(
+        16 * blk + __popcll(__ballot(lane < 16 && tt.end[16 * blk + (lane & 15)] <= mt)));
     const int first = g > 0 ? tt.end[g - 1] : 0, n = tt.end[g] - first;
     const int local = v - first * tiles_n;
-    Tile t;
-    t.g = __builtin_amdgcn_readfirstlane(g);
-    t.m0 = __builtin_amdgcn_readfirstlane((local % n) * bm);
-    t.nt = __builtin_amdgcn_readfirstlane(local / n);
-    const int lo = __builtin_amdgcn_readfirstlane(tt.lo[g]);
-    t.base = lo;
-    t.Mg = __builtin_amdgcn_readfirstlane(tt.hi[g]) - lo;
-    t.Kg = 0;
+    TileAt t;
+    t.g = g;
+    t.n0 = __builtin_amdgcn_readfirstlane(local / n * BN);
+    t.row = __builtin_amdgcn_readfirstlane(tt.lo[g] + local % n * BM);
+    t.rows = __builtin_amdgcn_readfirstlane(local % n == n - 1 ? static_cast<int>(tt.last[g]) : BM);
     return t;
 }
 
@@ -475,16 +483,17 @@ __device__ __forceinline__ Tile find_tile(const TileTable &tt, int v, int tiles_
 template <int NB, bool MAP>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx8_tile_kernel(Mx8Args p) {
     constexpr int BM = 256, BN = 256 / NB, WGN = 2, NW = 4, S = 2;
-    constexpr int WTM = 128, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32, TT = NB * TN;
-    static_assert(TM == 4 && TT == 4, "sixteen 32 x 32 results a wave");
+    constexpr int WTM = 128, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32;
+    static_assert(TM == 4 && NB * TN == 4, "sixteen 32 x 32 results a wave");
     constexpr int kABytes = BM * 128, kBBytes = BN * 128, kStage = kABytes + NB * kBBytes;
     constexpr int kL = kStage / (NW * 1024);  // operand loads of a wave per block
     static_assert(kL == 16, "seven in step 0, nine in step 1");
     constexpr int kScales = 512 * 4;          // scale dwords of 256 + 256 rows
     constexpr int kRing = S * kStage;
-    static_assert(kRing + S * kScales + sizeof(TileTable) <= 160 * 1024, "one block per compute unit");
+    static_assert(kRing + S * kScales + sizeof(TileTable) + 4 * 4096 <= 160 * 1024, "one block per compute unit");
     __shared__ __align__(1024) char smem[kRing + S * kScales];
     __shared__ TileTable tt;
+    __shared__ __align__(16) char stage[NB == 1 ? 4 * 4096 : 16];
 
     const int N = p.g.N, K = p.K, kb = (K + 127) / 128, kbe = max(kb, 2);  // blocks, two at least
     const int tiles_n = (N + BN - 1) / BN;
@@ -495,7 +504,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     const uint32_t sbase = __builtin_amdgcn_readfirstlane(lds_addr(smem));
     int v = blockIdx.x;
     if (v >= tiles) return;
-    Tile t = find_tile(tt, xcd_tile_order(v, tiles), tiles_n, BM);
+    // Tile of turn v: runs of consecutive tiles to an XCD as in xcd_tile_order
+    // (this grid's 32 blocks of an XCD make a run in each round), turned by one
+    // from round to round: an expert's last row tile is often shorter, and with
+    // two row tiles an expert the same blocks would have all the long ones.
+    auto turn = [&](int u) {
+        constexpr int W = kXcds * kXcdRun;
+        static_assert(kComputeUnits == W, "a round is one run on each XCD");
+        const int round = u / W, b = u % W;
+        if (round >= tiles / W) return u;
+        return round * W + b % kXcds * kXcdRun + (b / kXcds + round) % kXcdRun;
+    };
+    TileAt t = find_tile<BM, BN>(tt, turn(v), tiles_n);
 
     // Operand loads: load i of wave w fills tile rows 32 i + 8 w .. + 7, lane l
     // the chunk l % 8 of row 8 w + l / 8, which holds the row's chunk c (the
@@ -511,10 +531,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         __amdgpu_buffer_rsrc_t a, b0, b1, as, bs;
         uint32_t aoff[MAP ? 8 : 1], as_off, bs_off;
     };
-    auto source = [&](const Tile &u) {
+    auto source = [&](const TileAt &u) {
         Source q;
-        const int rows = u.Mg - u.m0, n0 = u.nt * BN;
-        const int64_t r0 = u.base + u.m0;
+        const int rows = u.rows, n0 = u.n0;
+        const int64_t r0 = u.row;
         const int m = 64 * wave + lane;  // scales: wave w takes rows 64 w .. + 63 of A's 256 and of B's
         q.as_off = m < rows ? 4u * m : kOut;
         if constexpr (MAP) {
@@ -532,7 +552,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             q.a = make_rsrc(p.a, p.a_rows * K);
             q.as = make_rsrc(p.as, p.a_rows * kb * 4);
         } else {
-            q.a = make_rsrc(p.a + r0 * K, static_cast<int64_t>(min(rows, BM)) * K);
+            q.a = make_rsrc(p.a + r0 * K, static_cast<int64_t>(rows) * K);
             q.as = make_rsrc(p.as + r0 * 4, (p.a_rows * kb - r0) * 4);
         }
         const int64_t b_at = (static_cast<int64_t>(u.g) * N + n0) * K;
@@ -587,38 +607,26 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 #pragma unroll
     for (int c = 0; c < 4; ++c) fad[c] = row * 128 + 16 * ((2 * c + half) ^ sw);
     f32x16_t acc[NB][TM][TN];
-    i32x8_t fA[2][TM], fB[2][TT];
-    int sA[2][TM], sB[2][TT];
+    i32x8_t fA[2][TM], fB[2][4];
+    int sA[2][TM], sB[2][4];
     typedef __attribute__((address_space(3))) const i32x4_t lds_i32x4;
     struct Frags {  // addresses of a step's fragments: one add each, the rest immediates
         uint32_t alo, ahi, blo, bhi;
     };
-    auto frags = [&](int s, int slot) {
-        const uint32_t sa = sbase + slot * kStage + wm * WTM * 128;
-        const uint32_t sb = sbase + slot * kStage + kABytes + wn * WTN * 128;
+    auto frags = [&](int s, int slot, int arow, int bcol) {
+        const uint32_t sa = sbase + slot * kStage + arow * 128;
+        const uint32_t sb = sbase + slot * kStage + kABytes + bcol * 128;
         return Frags{fresh(sa + fad[2 * s]), fresh(sa + fad[2 * s + 1]), fresh(sb + fad[2 * s]), fresh(sb + fad[2 * s + 1])};
     };
-    auto read_unit = [&](const Frags &f, int s, int u) {  // fragment u of step s
-        const uint32_t off = u < TM ? 32 * u * 128 : ((u - TM) / TN) * kBBytes + 32 * ((u - TM) % TN) * 128;
-        const i32x4_t lo = *reinterpret_cast<lds_i32x4 *>(static_cast<uintptr_t>((u < TM ? f.alo : f.blo) + off));
-        const i32x4_t hi = *reinterpret_cast<lds_i32x4 *>(static_cast<uintptr_t>((u < TM ? f.ahi : f.bhi) + off));
-        const i32x8_t v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        if (u < TM) fA[s][u] = v;
-        else fB[s][u - TM] = v;
+    auto read_a = [&](const Frags &f, int s, int i) {
+        const i32x4_t lo = *reinterpret_cast<lds_i32x4 *>(static_cast<uintptr_t>(f.alo + 4096 * i));
+        const i32x4_t hi = *reinterpret_cast<lds_i32x4 *>(static_cast<uintptr_t>(f.ahi + 4096 * i));
+        fA[s][i] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     };
-    auto read_scales = [&](int set, int slot) {
-        const uint32_t ss = sbase + kRing + slot * kScales;
-        const uint32_t sa = fresh(ss + (wm * WTM + row) * 4), sb = fresh(ss + 1024 + (wn * WTN + row) * 4);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) sA[set][i] = lds_read_i32(sa + 128 * i) >> (8 * half);
-#pragma unroll
-        for (int u = 0; u < TT; ++u) sB[set][u] = lds_read_i32(sb + 4 * (u / TN) * BN + 128 * (u % TN)) >> (8 * half);
-    };
-    auto read_first = [&](int slot) {
-        read_scales(0, slot);
-        const Frags f = frags(0, slot);
-#pragma unroll
-        for (int u = 0; u < TM + TT; ++u) read_unit(f, 0, u);
+    auto read_b = [&](const Frags &f, int s, int u, int off) {
+        const i32x4_t lo = *reinterpret_cast<lds_i32x4 *>(static_cast<uintptr_t>(f.blo + off));
+        const i32x4_t hi = *reinterpret_cast<lds_i32x4 *>(static_cast<uintptr_t>(f.bhi + off));
+        fB[s][u] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     };
 
     Source src = source(t);
@@ -635,140 +643,200 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     while (true) {
         const int nv = v + static_cast<int>(gridDim.x);
         const bool more = nv < tiles;
-        const Tile next = more ? find_tile(tt, xcd_tile_order(nv, tiles), tiles_n, BM) : t;
+        const TileAt next = more ? find_tile<BM, BN>(tt, turn(nv), tiles_n) : t;
         const Source nsrc = source(next);
-        const int m0 = t.m0, n0 = t.nt * BN;
-        read_first(slot);
+        // One tile.  HALF: at most 128 rows, which all four waves share, each with
+        // half the columns it has otherwise (128 x 64 of the 128 x 256 results).
+        auto tile = [&](auto half_tag) {
+            constexpr bool HALF = decltype(half_tag)::value;
+            constexpr int TJ = HALF ? TN / 2 : TN;        // column blocks of 32 of each matrix
+            constexpr int TT = NB * TJ, NQ = TM * TT;     // B fragments, products of a step
+            const int arow = HALF ? 0 : wm * WTM;
+            const int bcol = HALF ? wave * 32 * TJ : wn * WTN;
+            // fragment u of B: matrix u / TJ, column block u % TJ
+            auto read_unit = [&](const Frags &f, int s, int u) {
+                if (u < TM) read_a(f, s, u);
+                else read_b(f, s, u - TM, ((u - TM) / TJ) * kBBytes + ((u - TM) % TJ) * 4096);
+            };
+            auto read_scales = [&](int set, int sl) {
+                const uint32_t ss = sbase + kRing + sl * kScales;
+                const uint32_t sa = fresh(ss + (arow + row) * 4), sb = fresh(ss + 1024 + (bcol + row) * 4);
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+                for (int i = 0; i < TM; ++i) sA[set][i] = lds_read_i32(sa + 128 * i) >> (8 * half);
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+                for (int u = 0; u < TT; ++u) sB[set][u] = lds_read_i32(sb + 4 * (u / TJ) * BN + 128 * (u % TJ)) >> (8 * half);
+            };
+            {
+                read_scales(0, slot);
+                const Frags f = frags(0, slot, arow, bcol);
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[b][i][j][r] = 0.0f;
-        // product q of step s.  The order around it is pinned: left to itself
-        // the compiler puts all reads in front of the products, which then
-        // wait for shared memory.
-        auto product = [&](int s, int q) {
-            const int u = q / TM, i = q % TM;
-            if (s == 0)
-                acc[u / TN][i][u % TN] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    fB[0][u], fA[0][i], acc[u / TN][i][u % TN], 0, 0, 0, sB[0][u], 0, sA[0][i]);
-            else
-                acc[u / TN][i][u % TN] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    fB[1][u], fA[1][i], acc[u / TN][i][u % TN], 0, 0, 2, sB[0][u], 2, sA[0][i]);
-        };
-        for (int blk = 0; blk < kbe; ++blk) {
-            const bool ahead = blk + 2 >= kbe;  // the loads are the next tile's first two blocks
-            if (blk + 2 == kbe) src = nsrc;
-            const Plan pl = plan(ahead ? blk + 2 - kbe : blk + 2, !ahead || more);
-            const Frags f1 = frags(1, slot);
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                product(0, q);
-                if (q < TM + TT) read_unit(f1, 1, q);
-                if (q == 8) {
-                    __syncthreads();  // every wave has read this block: its slot is free
-                    issue_scales(src, pl, slot);
-                }
-                if (q > 8) issue_part(src, pl, slot, q - 9);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            wait_vmem<2 + 7>();  // the next block has landed (what is out is of the one after)
-            __syncthreads();
-            read_scales(1, slot ^ 1);
-            const Frags f0 = frags(0, slot ^ 1);
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                product(1, q);
-                if (q < TM + TT) read_unit(f0, 0, q);
-                if (q < 9) issue_part(src, pl, slot, q + 7);
-                __builtin_amdgcn_sched_barrier(0);
+                for (int u = 0; u < TM + TT; ++u) read_unit(f, 0, u);
             }
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                sA[0][i] = sA[1][i];
-                sB[0][i] = sB[1][i];
-            }
-            slot ^= 1;
-        }
-        // the sums stay in the accumulation registers until their turn
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+                for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+                    for (int j = 0; j < TJ; ++j)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[b][i][j]));
-        // lane l: row 32 i + l % 32, columns 32 j + 8 g + 4 (l / 32) + r.  Swapping
-        // the lanes' halves gives each 16 consecutive bytes of its row.  Stores go
-        // through buffers that end with the group's rows and with bit 31 set past
-        // N, so that nothing branches and each result stays in its accumulator
-        // until its turn.
-        const int64_t r0 = t.base + m0;
-        const int rows = min(t.Mg - m0, BM);
-        typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-        const int erow = static_cast<int>(fresh(wm * WTM + row));
-        if constexpr (NB == 1) {
-            const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.y + r0 * N, static_cast<int64_t>(rows) * N * 2);
+                        for (int r = 0; r < 16; ++r) acc[b][i][j][r] = 0.0f;
+            // product q of step s.  The order around it is pinned: left to itself
+            // the compiler puts all reads in front of the products, which then
+            // wait for shared memory.
+            auto product = [&](int s, int q) {
+                const int u = q / TM, i = q % TM;
+                if (s == 0)
+                    acc[u / TJ][i][u % TJ] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        fB[0][u], fA[0][i], acc[u / TJ][i][u % TJ], 0, 0, 0, sB[0][u], 0, sA[0][i]);
+                else
+                    acc[u / TJ][i][u % TJ] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        fB[1][u], fA[1][i], acc[u / TJ][i][u % TJ], 0, 0, 2, sB[0][u], 2, sA[0][i]);
+            };
+            constexpr int kParts0 = 7;             // loads in step 0, the rest in step 1
+            constexpr int kBar = HALF ? 4 : 8;     // the product whose turn frees the slot
+            for (int blk = 0; blk < kbe; ++blk) {
+                const bool ahead = blk + 2 >= kbe;  // the loads are the next tile's first two blocks
+                if (blk + 2 == kbe) src = nsrc;
+                const Plan pl = plan(ahead ? blk + 2 - kbe : blk + 2, !ahead || more);
+                const Frags f1 = frags(1, slot, arow, bcol);
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    const int c = n0 + wn * WTN + 32 * j;
-                    const uint32_t at = static_cast<uint32_t>((erow + 32 * i) * N + c + 8 * half) * 2u;
-#pragma unroll
-                    for (int g = 0; g < 4; g += 2) {
-                        const f32x16_t &a = acc[0][i][j];
-                        const auto x = __builtin_amdgcn_permlane32_swap(
-                            cvt_bf16x2(a[4 * g], a[4 * g + 1]), cvt_bf16x2(a[4 * g + 4], a[4 * g + 5]), false, false);
-                        const auto y = __builtin_amdgcn_permlane32_swap(
-                            cvt_bf16x2(a[4 * g + 2], a[4 * g + 3]), cvt_bf16x2(a[4 * g + 6], a[4 * g + 7]), false, false);
-                        __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{x[0], y[0], x[1], y[1]}, ry,
-                                                               static_cast<int>(c < N ? at + 16u * g : kOut), 0, 0);
+                for (int q = 0; q < NQ; ++q) {
+                    product(0, q);
+                    if constexpr (HALF) {
+                        if (q < 3) {
+                            read_unit(f1, 1, 2 * q);
+                            read_unit(f1, 1, 2 * q + 1);
+                        }
+                    } else {
+                        if (q < TM + TT) read_unit(f1, 1, q);
                     }
-                    __builtin_amdgcn_sched_barrier(0);  // one 32 x 32 result at a time: registers
-                }
-        } else {
-            const __amdgpu_buffer_rsrc_t rq = make_rsrc(p.q + r0 * N, static_cast<int64_t>(rows) * N);
-            const __amdgpu_buffer_rsrc_t rs =
-                make_rsrc(p.qs + (static_cast<int64_t>(n0 / 128) * p.g.extent + r0) * 4, rows * 4);
-#pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const int m = erow + 32 * i;
-                uint32_t bytes = 0u;
-#pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    const int c = n0 + wn * WTN + 32 * j;
-                    f32x16_t h1 = acc[0][i][j], h3 = acc[1][i][j];
-                    asm volatile("" : "+v"(h1), "+v"(h3));
-                    float o[16];
-                    uint32_t a = 0u;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        o[e] = h1[e] * __builtin_amdgcn_rcpf(1.0f + __expf(-h1[e])) * h3[e];
-                        a = max(a, __float_as_uint(o[e]) & 0x7fffffffu);
+                    if (q == kBar) {
+                        __syncthreads();  // every wave has read this block: its slot is free
+                        issue_scales(src, pl, slot);
                     }
-                    const auto other = __builtin_amdgcn_permlane32_swap(a, a, false, false);
-                    a = max(other[0], other[1]);
-                    const uint32_t byte = mx8_scale_byte(a);
-                    const float s = mx8_inv_scale(byte);
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        w[e / 4] = mx8_pack4(o[e] * s, o[e + 1] * s, o[e + 2] * s, o[e + 3] * s);
-                    const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-                    const auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-                    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{x[0], x[1], y[0], y[1]}, rq,
-                                                           static_cast<int>(c < N ? m * N + c + 16 * half : kOut), 0, 0);
-                    // past N: the byte that fills the last group (a NaN row is NaN there too)
-                    bytes |= (c < N ? byte : kMxOne) << (8 * j);
+                    if constexpr (HALF) {
+                        if (q > kBar) {
+                            issue_part(src, pl, slot, 2 * (q - kBar - 1));
+                            issue_part(src, pl, slot, 2 * (q - kBar - 1) + 1);
+                            if (q == NQ - 1) issue_part(src, pl, slot, 6);
+                        }
+                    } else {
+                        if (q > kBar) issue_part(src, pl, slot, q - kBar - 1);
+                    }
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(bytes), rs,
-                                                      static_cast<int>(half ? kOut : m * 4u + 2u * wn), 0, 0);
+                wait_vmem<2 + kParts0>();  // the next block has landed (what is out is of the one after)
+                __syncthreads();
+                read_scales(1, slot ^ 1);
+                const Frags f0 = frags(0, slot ^ 1, arow, bcol);
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    product(1, q);
+                    if constexpr (HALF) {
+                        if (q < TM + TT) read_unit(f0, 0, q);
+                        if (q < 4) issue_part(src, pl, slot, kParts0 + 2 * q + 1);
+                        if (q < 5) issue_part(src, pl, slot, kParts0 + 2 * q);
+                    } else {
+                        if (q % 2 == 0) read_unit(f0, 0, q / 2);
+                        if (q < kL - kParts0) issue_part(src, pl, slot, q + kParts0);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int i = 0; i < TM; ++i) sA[0][i] = sA[1][i];
+#pragma unroll
+                for (int u = 0; u < TT; ++u) sB[0][u] = sB[1][u];
+                slot ^= 1;
             }
-        }
+            // the sums stay in the accumulation registers until their turn
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TJ; ++j) asm volatile("" : "+a"(acc[b][i][j]));
+            // lane l: row 32 i + l % 32, columns 32 j + 8 g + 4 (l / 32) + r.  Stores go
+            // through buffers that end with the tile's rows and with bit 31 set past
+            // N, so that nothing branches and each result stays in its accumulator
+            // until its turn.
+            typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+            if constexpr (NB == 1) {
+                // 32 rows by 64 columns at a time through a piece of shared memory of
+                // the wave's own (chunk c of row m at c ^ (m % 8)): the stores then
+                // cover 128 consecutive bytes of a row instead of 32 (down-projection
+                // of 131072 rows, d = 4096, h = 1024: 655 -> 610 us)
+                char *const st = stage + wave * 4096;
+                const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.y + t.row * N, static_cast<int64_t>(t.rows) * N * 2);
+                const int wrow = static_cast<int>(fresh(row)), rrow = static_cast<int>(fresh(lane >> 3)), rch = lane & 7;
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TJ; j += 2) {
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) {
+                            const f32x16_t &a = acc[0][i][j + g / 4];
+                            const int e = 4 * (g % 4);
+                            *reinterpret_cast<uint2 *>(st + wrow * 128 + 16 * (g ^ (wrow & 7)) + 8 * half) =
+                                make_uint2(cvt_bf16x2(a[e], a[e + 1]), cvt_bf16x2(a[e + 2], a[e + 3]));
+                        }
+                        __builtin_amdgcn_wave_barrier();
+                        const int c = t.n0 + bcol + 32 * j + 8 * rch;
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            const int m = 8 * h + rrow;
+                            const u32x4_t v = *reinterpret_cast<const u32x4_t *>(st + m * 128 + 16 * (rch ^ (m & 7)));
+                            const uint32_t at = static_cast<uint32_t>((arow + 32 * i + m) * N + c) * 2u;
+                            __builtin_amdgcn_raw_buffer_store_b128(v, ry, static_cast<int>(c < N ? at : kOut), 0, 0);
+                        }
+                        __builtin_amdgcn_wave_barrier();
+                        __builtin_amdgcn_sched_barrier(0);  // one piece at a time: registers
+                    }
+            } else {
+                // swapping the lanes' halves gives each 16 consecutive bytes of its row
+                const __amdgpu_buffer_rsrc_t rq = make_rsrc(p.q + t.row * N, static_cast<int64_t>(t.rows) * N);
+                const __amdgpu_buffer_rsrc_t rs =
+                    make_rsrc(p.qs + (static_cast<int64_t>(t.n0 / 128) * p.g.extent + t.row) * 4, t.rows * 4);
+                const int erow = static_cast<int>(fresh(arow + row));
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const int m = erow + 32 * i;
+                    uint32_t bytes = 0u;
+#pragma unroll
+                    for (int j = 0; j < TJ; ++j) {
+                        const int c = t.n0 + bcol + 32 * j;
+                        f32x16_t h1 = acc[0][i][j], h3 = acc[1][i][j];
+                        asm volatile("" : "+v"(h1), "+v"(h3));
+                        float o[16];
+                        uint32_t a = 0u;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            o[e] = h1[e] * __builtin_amdgcn_rcpf(1.0f + __expf(-h1[e])) * h3[e];
+                            a = max(a, __float_as_uint(o[e]) & 0x7fffffffu);
+                        }
+                        const auto other = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+                        a = max(other[0], other[1]);
+                        const uint32_t byte = mx8_scale_byte(a);
+                        const float s = mx8_inv_scale(byte);
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            w[e / 4] = mx8_pack4(o[e] * s, o[e + 1] * s, o[e + 2] * s, o[e + 3] * s);
+                        const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+                        const auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+                        __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{x[0], x[1], y[0], y[1]}, rq,
+                                                               static_cast<int>(c < N ? m * N + c + 16 * half : kOut), 0, 0);
+                        // past N: the byte that fills the last group (a NaN row is NaN there too)
+                        bytes |= (c < N ? byte : kMxOne) << (8 * j);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    const int at = static_cast<int>(half ? kOut : m * 4u + bcol / 32u);
+                    if constexpr (HALF) __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(bytes), rs, at, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(bytes), rs, at, 0, 0);
+                }
+            }
+        };
+        if (t.rows <= WTM) tile(std::true_type{});
+        else tile(std::false_type{});
         if (!more) break;
         t = next;
         v = nv;
