@@ -389,6 +389,14 @@ __device__ __forceinline__ void lds_dma4(__amdgpu_buffer_rsrc_t rs, uint32_t vof
                  : "memory");
 }
 
+// A buffer over `bytes` from `base`; none where there is nothing (offsets with
+// bit 31 set must be out of range, so a size never wraps).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t over(const void *base, int64_t bytes) {
+    return make_rsrc(base, bytes > 0 ? bytes : 0);
+}
+
+// The tiles of a launch, found from the device-side offsets once per block and
+// kept in shared memory.
 struct TileTable {
     int end[1024];        // row tiles up to and including the expert's; INT_MAX past the last expert
     int lo[1024];         // first row
@@ -502,20 +510,34 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WGN, wn = wave % WGN, half = lane >> 5;
     const uint32_t sbase = __builtin_amdgcn_readfirstlane(lds_addr(smem));
-    int v = blockIdx.x;
-    if (v >= tiles) return;
-    // Tile of turn v: runs of consecutive tiles to an XCD as in xcd_tile_order
-    // (this grid's 32 blocks of an XCD make a run in each round), turned by one
-    // from round to round: an expert's last row tile is often shorter, and with
-    // two row tiles an expert the same blocks would have all the long ones.
-    auto turn = [&](int u) {
-        constexpr int W = kXcds * kXcdRun;
-        static_assert(kComputeUnits == W, "a round is one run on each XCD");
+    // Turn u of the launch.  Runs of consecutive tiles to an XCD as in
+    // xcd_tile_order (this grid's 32 blocks of an XCD make a run in each round),
+    // turned by one from round to round: an expert's last row tile is often
+    // shorter, and with two row tiles an expert the same blocks would have all
+    // the long ones.  Where the last round has tiles for at most half the blocks,
+    // two blocks take 128 rows each of one.
+    constexpr int W = kXcds * kXcdRun;
+    static_assert(kComputeUnits == W, "a round is one run on each XCD");
+    const int whole = tiles / W * W, rest = tiles - whole;
+    const bool split = 2 * rest <= W;
+    const int turns = whole + (split ? 2 * rest : rest);
+    auto take = [&](int u) {
         const int round = u / W, b = u % W;
-        if (round >= tiles / W) return u;
-        return round * W + b % kXcds * kXcdRun + (b / kXcds + round) % kXcdRun;
+        if (u < whole)
+            return find_tile<BM, BN>(tt, round * W + b % kXcds * kXcdRun + (b / kXcds + round) % kXcdRun, tiles_n);
+        TileAt t = find_tile<BM, BN>(tt, split ? whole + (u - whole) / 2 : u, tiles_n);
+        if (split) {
+            // a short tile's second half is empty: it starts at its end, never behind
+            // the rows, so that no buffer's size goes below zero
+            const int from = min((u - whole) % 2 * WTM, t.rows);
+            t.row += from;
+            t.rows = min(t.rows - from, WTM);
+        }
+        return t;
     };
-    TileAt t = find_tile<BM, BN>(tt, turn(v), tiles_n);
+    int v = blockIdx.x;
+    if (v >= turns) return;
+    TileAt t = take(v);
 
     // Operand loads: load i of wave w fills tile rows 32 i + 8 w .. + 7, lane l
     // the chunk l % 8 of row 8 w + l / 8, which holds the row's chunk c (the
@@ -549,20 +571,20 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             }
             const int id = id_of(m);
             q.as_off = id >= 0 ? 4u * id : kOut;
-            q.a = make_rsrc(p.a, p.a_rows * K);
-            q.as = make_rsrc(p.as, p.a_rows * kb * 4);
+            q.a = over(p.a, p.a_rows * K);
+            q.as = over(p.as, p.a_rows * kb * 4);
         } else {
-            q.a = make_rsrc(p.a + r0 * K, static_cast<int64_t>(rows) * K);
-            q.as = make_rsrc(p.as + r0 * 4, (p.a_rows * kb - r0) * 4);
+            q.a = over(p.a + r0 * K, static_cast<int64_t>(rows) * K);
+            q.as = over(p.as + r0 * 4, (p.a_rows * kb - r0) * 4);
         }
         const int64_t b_at = (static_cast<int64_t>(u.g) * N + n0) * K;
         const int64_t bbytes = static_cast<int64_t>(min(N - n0, BN)) * K;
-        q.b0 = make_rsrc(p.b0 + b_at, bbytes);
-        q.b1 = make_rsrc((NB == 2 ? p.b1 : p.b0) + b_at, bbytes);
+        q.b0 = over(p.b0 + b_at, bbytes);
+        q.b1 = over((NB == 2 ? p.b1 : p.b0) + b_at, bbytes);
         const int col = NB == 2 ? m & 127 : m;  // B's: of W1 and W3 128 each
         q.bs_off = n0 + col < N ? 4u * col : kOut;
         const int64_t bs_at = static_cast<int64_t>(u.g) * kb * N + n0;
-        q.bs = make_rsrc(((NB == 2 && wave >= 2) ? p.b1s : p.b0s) + bs_at * 4, (static_cast<int64_t>(kb) * N - n0) * 4);
+        q.bs = over(((NB == 2 && wave >= 2) ? p.b1s : p.b0s) + bs_at * 4, (static_cast<int64_t>(kb) * N - n0) * 4);
         return q;
     };
     // blocks past the end load zeros, so that the count of loads in flight stays the same
@@ -642,8 +664,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     int slot = 0;
     while (true) {
         const int nv = v + static_cast<int>(gridDim.x);
-        const bool more = nv < tiles;
-        const TileAt next = more ? find_tile<BM, BN>(tt, turn(nv), tiles_n) : t;
+        const bool more = nv < turns;
+        const TileAt next = more ? take(nv) : t;
         const Source nsrc = source(next);
         // One tile.  HALF: at most 128 rows, which all four waves share, each with
         // half the columns it has otherwise (128 x 64 of the 128 x 256 results).
@@ -766,7 +788,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
                 // cover 128 consecutive bytes of a row instead of 32 (down-projection
                 // of 131072 rows, d = 4096, h = 1024: 655 -> 610 us)
                 char *const st = stage + wave * 4096;
-                const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.y + t.row * N, static_cast<int64_t>(t.rows) * N * 2);
+                const __amdgpu_buffer_rsrc_t ry = over(p.y + t.row * N, static_cast<int64_t>(t.rows) * N * 2);
                 const int wrow = static_cast<int>(fresh(row)), rrow = static_cast<int>(fresh(lane >> 3)), rch = lane & 7;
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
@@ -793,9 +815,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
                     }
             } else {
                 // swapping the lanes' halves gives each 16 consecutive bytes of its row
-                const __amdgpu_buffer_rsrc_t rq = make_rsrc(p.q + t.row * N, static_cast<int64_t>(t.rows) * N);
+                const __amdgpu_buffer_rsrc_t rq = over(p.q + t.row * N, static_cast<int64_t>(t.rows) * N);
                 const __amdgpu_buffer_rsrc_t rs =
-                    make_rsrc(p.qs + (static_cast<int64_t>(t.n0 / 128) * p.g.extent + t.row) * 4, t.rows * 4);
+                    over(p.qs + (static_cast<int64_t>(t.n0 / 128) * p.g.extent + t.row) * 4, t.rows * 4);
                 const int erow = static_cast<int>(fresh(arow + row));
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
@@ -848,7 +870,7 @@ template <int NB, bool MAP>
 hipError_t launch_tile(const Mx8Args &p, hipStream_t s) {
     constexpr int BM = 256, BN = 256 / NB;
     const int64_t tiles = p.g.extent / BM + std::min<int64_t>(p.g.G, p.g.extent);
-    const int64_t grid = std::min<int64_t>(tiles * ((p.g.N + BN - 1) / BN), kComputeUnits);
+    const int64_t grid = std::min<int64_t>(2 * tiles * ((p.g.N + BN - 1) / BN), kComputeUnits);
     if (grid <= 0) return hipSuccess;
     hipLaunchKernelGGL((mx8_tile_kernel<NB, MAP>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
     return hipGetLastError();

@@ -188,7 +188,9 @@ def _check_experts(xm, counts, d, h, T=None, seed=0, spare=0, tweak=None):
     ([1], 32, 32, None), ([1], 128, 32, 1), ([0, 3, 0], 96, 64, 5), ([17, 0, 16, 15], 160, 96, 20),
     ([33, 1, 31, 32, 64], 288, 160, None), ([5, 0, 0, 200, 7], 256, 224, 100), ([300], 128, 1056, 64),
     ([129, 127, 128], 544, 128, 50), ([2, 1, 0, 1, 0, 0, 2, 1], 2048, 1408, 1), ([257, 511, 256, 0, 3], 384, 416, 700),
-    ([1030, 70], 64, 640, 300), ([600, 900], 1024, 256, None)])
+    ([1030, 70], 64, 640, 300), ([600, 900], 1024, 256, None),
+    # row tiles whose second 128 rows are empty, at the end of the rows, with one 128-deep step
+    ([300, 260], 96, 128, None), ([300, 260], 128, 96, None), ([257, 1, 513], 64, 32, None), ([4, 900, 257], 128, 160, 90)])
 def test_experts(xm, counts, d, h, T):
     print(f"[experts8] counts={counts} d={d} h={h} T={T}", flush=True)
     _check_experts(xm, counts, d, h, T, seed=len(counts) + d)
