@@ -28,11 +28,11 @@ namespace {
 
 constexpr int kWaves = 4;
 
-// Tokens per block: about 1024 blocks, four on each compute unit, at least one
+// Tokens per block: about 2048 blocks, eight on each compute unit, at least one
 // step of every wave; at most 128, so that a sum of p has few terms in sequence
 inline int chunk_tokens(int64_t T) {
     int c = 16;
-    while (c < 128 && T > static_cast<int64_t>(c) * 1024) c *= 2;
+    while (c < 128 && T > static_cast<int64_t>(c) * 2048) c *= 2;
     return c;
 }
 // experts per block of the second kernel: its 32 row groups share a sequence's rows
@@ -90,18 +90,26 @@ __device__ __forceinline__ void load_token(const float *row, bool live, int r, i
     }
 }
 
-// Logits -> probabilities in place (dead tokens: 0).  One division a token.
+// Logits -> probabilities in place (dead tokens: 0).  exp(x - max) is taken as
+// 2^(x L - max L), L = log2(e), with one fused multiply-add: the rounding of
+// max L is the same factor in every term and leaves with the division, so the
+// error is that of the exponent's one rounding, |x - max| 2^-24, as with the
+// difference taken first.  (With expf and its range checks the arithmetic, not
+// the loads, bound these kernels: 44 vector instructions an element.)  One
+// division a token.
 template <int LT, int QQ>
-__device__ __forceinline__ void token_softmax(bool live, int r, int E, float (&p)[QQ]) {
+__device__ __forceinline__ void token_softmax(bool live, float (&p)[QQ]) {
+    constexpr float kLog2e = 1.44269504f;
     float mx = -INFINITY;
 #pragma unroll
     for (int q = 0; q < QQ; ++q) mx = fmaxf(mx, p[q]);
 #pragma unroll
     for (int off = LT / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+    const float shift = -mx * kLog2e;
     float den = 0.0f;
 #pragma unroll
-    for (int q = 0; q < QQ; ++q) {
-        p[q] = 4 * (r + LT * (q >> 2)) + (q & 3) < E && live ? expf(p[q] - mx) : 0.0f;
+    for (int q = 0; q < QQ; ++q) {  // 0 past E, where the logits are -infinity
+        p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[q], kLog2e, shift));
         den += p[q];
     }
 #pragma unroll
@@ -127,6 +135,13 @@ __global__ __launch_bounds__(64 * kWaves) void balance_part_kernel(const float *
     const int64_t t1 = t0 + chunk < T ? t0 + chunk : T;
     if (blockIdx.x == 0 && threadIdx.x == 0) *ws.ticket = 0;
     auto ex = [&](int q) { return 4 * (r + LT * (q >> 2)) + (q & 3); };
+    // the first step's logits are on their way during the search: the first piece
+    // starts with the chunk unless the chunk starts in front of the first sequence
+    float next[QQ];
+    load_token<LT, QQ>(logits + (t0 + slot) * E, t0 + slot < T, r, E, next);
+    int nid = t0 + slot < T && r < k ? ids[(t0 + slot) * k + r] : -1;
+    uint8_t nmask = mask && t0 + slot < T ? mask[t0 + slot] : 1;
+    bool ahead = true;
     // the sequences that this chunk meets, in order (the same in every thread)
     int s = 0;
     if (off) s = max(find_sequence<64>(off, S, t0), 0);
@@ -147,22 +162,22 @@ __global__ __launch_bounds__(64 * kWaves) void balance_part_kernel(const float *
         for (int q = 0; q < QQ; ++q) acc[q] = 0.0f;
         __syncthreads();
         // the next step's logits are on their way while this one's are worked on
-        float next[QQ];
-        auto counted = [&](int64_t t) { return t < hi && (!mask || mask[t] != 0); };
-        bool nlive = counted(lo + slot);
-        int nid = nlive && r < k ? ids[(lo + slot) * k + r] : -1;
-        load_token<LT, QQ>(logits + (lo + slot) * E, nlive, r, E, next);
+        auto ask = [&](int64_t t) {
+            nmask = mask && t < hi ? mask[t] : 1;
+            nid = t < hi && r < k ? ids[t * k + r] : -1;
+            load_token<LT, QQ>(logits + t * E, t < hi, r, E, next);
+        };
+        if (!(ahead && lo == t0)) ask(lo + slot);
+        ahead = false;
         for (int64_t tb = lo; tb < hi; tb += TPB) {
             const int64_t t = tb + slot;
-            const bool live = nlive;
+            const bool live = t < hi && nmask != 0;
+            const int id = nid;
             float p[QQ];
 #pragma unroll
             for (int q = 0; q < QQ; ++q) p[q] = next[q];
-            const int id = nid;
-            nlive = counted(t + TPB);
-            nid = nlive && r < k ? ids[(t + TPB) * k + r] : -1;
-            load_token<LT, QQ>(logits + (t + TPB) * E, nlive, r, E, next);
-            token_softmax<LT, QQ>(live, r, E, p);
+            ask(t + TPB);
+            token_softmax<LT, QQ>(live, p);
 #pragma unroll
             for (int q = 0; q < QQ; ++q) acc[q] += p[q];
             if (live) {
@@ -217,30 +232,17 @@ __device__ __forceinline__ void piece_rows(const int32_t *off, int s, int64_t T,
     *hi = a < b ? (b - 1) / chunk + s + 1 : 0;
 }
 
-template <typename V>
-__device__ __forceinline__ V block_sum(V v, V *red) {  // 1024 threads, fixed order
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int w = 1; w < 16; ++w) v += red[w];
-    return v;
-}
-
 // A block per sequence and 32 experts.  The rows' values are asked for first;
 // what the counts need (n_s, S') comes beside them.
 __global__ __launch_bounds__(1024) void balance_final_kernel(int64_t T, int E, int k, const int32_t *off, int S,
                                                              int chunk, float alpha, BalanceWs ws, float *loss,
                                                              int32_t *counts, float *coef) {
-    __shared__ double red[16];
-    __shared__ int32_t redi[16];
-    __shared__ double sp[1024];
-    __shared__ int32_t sc[1024];
-    __shared__ int last;
+    __shared__ double red[32];
+    __shared__ int32_t wn[16], wsome[16];
+    __shared__ double sp[kFinalExperts][33];
+    __shared__ int32_t sc[kFinalExperts][33];
     constexpr int W = kFinalExperts, parts = 1024 / W;
+    static_assert(W == 32 && parts == 32, "half a wave for each expert");
     const int eb = static_cast<int>(gridDim.x) / S;  // blocks of a sequence
     const int s = blockIdx.x / eb;
     const int e = (blockIdx.x % eb) * W + threadIdx.x % W, part = threadIdx.x / W;
@@ -267,43 +269,72 @@ __global__ __launch_bounds__(1024) void balance_final_kernel(int64_t T, int E, i
             some += any;
         }
     }
-    sp[threadIdx.x] = p;
-    sc[threadIdx.x] = c;
-    n = block_sum(n, redi);
-    some = S > 1 ? block_sum(some, redi) : 1;
+    sp[threadIdx.x % W][part] = p;
+    sc[threadIdx.x % W][part] = c;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        n += __shfl_xor(n, o, 64);
+        some += __shfl_xor(some, o, 64);
+    }
+    if (threadIdx.x % 64 == 0) {
+        wn[threadIdx.x / 64] = n;
+        wsome[threadIdx.x / 64] = some;
+    }
+    __syncthreads();
+    n = 0;
+    some = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        n += wn[w];
+        some += wsome[w];
+    }
+    if (S == 1) some = 1;
+    // half a wave adds an expert's 32 row groups
+    const int re = (blockIdx.x % eb) * W + threadIdx.x / 32;
+    p = sp[threadIdx.x / 32][threadIdx.x % 32];
+    c = sc[threadIdx.x / 32][threadIdx.x % 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        p += __shfl_xor(p, o, 64);
+        c += __shfl_xor(c, o, 64);
+    }
     double l = 0.0;
-    if (part == 0 && e < E) {  // row groups in order
-        for (int i = 1; i < parts; ++i) {
-            p += sp[i * W + threadIdx.x];
-            c += sc[i * W + threadIdx.x];
-        }
+    if (threadIdx.x % 32 == 0 && re < E) {
         const double nn = n;
         const double f = n > 0 ? static_cast<double>(alpha) * E * c / (k * nn * nn * some) : 0.0;
-        counts[static_cast<int64_t>(s) * E + e] = c;
-        coef[static_cast<int64_t>(s) * E + e] = static_cast<float>(f);
+        counts[static_cast<int64_t>(s) * E + re] = c;
+        coef[static_cast<int64_t>(s) * E + re] = static_cast<float>(f);
         l = n > 0 ? f * p : 0.0;
     }
-    if (threadIdx.x < 64) {
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = l;
+    __syncthreads();
+    auto sum32 = [&](double v) {  // lanes 0 .. 31, in a fixed order
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor(l, o, 64);  // the 32 experts are in lanes 0 .. 31
-    }
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+        return v;
+    };
+    if (threadIdx.x >= 64) return;
+    l = sum32(red[threadIdx.x % 32]);
     if (gridDim.x == 1) {
         if (threadIdx.x == 0) *loss = static_cast<float>(l);
         return;
     }
-    // the last block to come adds the blocks' losses in order (the ticket was
-    // cleared by the kernel before); nobody waits for anybody
+    // The last block to come adds the blocks' losses in order (the ticket was
+    // cleared by the kernel before); nobody waits for anybody.  The loss is
+    // written through to where every XCD sees it and has arrived before the
+    // ticket is taken; nothing else is handed over, so no cache is flushed.
+    int got = 0;
     if (threadIdx.x == 0) {
         __hip_atomic_store(&ws.part_loss[blockIdx.x], l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const int got = __hip_atomic_fetch_add(ws.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-        last = got == static_cast<int>(gridDim.x) - 1;
+        __builtin_amdgcn_s_waitcnt(0);
+        got = __hip_atomic_fetch_add(ws.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    __syncthreads();
-    if (!last) return;
+    if (__shfl(got, 0, 64) != static_cast<int>(gridDim.x) - 1) return;
     l = 0.0;
-    for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += 1024)
-        l += __hip_atomic_load(&ws.part_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    l = block_sum(l, red);
+    if (threadIdx.x < 32)
+        for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += 32)
+            l += __hip_atomic_load(&ws.part_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    l = sum32(l);
     if (threadIdx.x == 0) *loss = static_cast<float>(l);
 }
 
@@ -315,11 +346,11 @@ __global__ __launch_bounds__(64 * kWaves) void balance_bwd_kernel(const float *_
     const int r = lane % LT;
     const int64_t t = (static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6)) * TPW + lane / LT;
     auto ex = [&](int q) { return 4 * (r + LT * (q >> 2)) + (q & 3); };
+    float p[QQ], g[QQ];
+    load_token<LT, QQ>(logits + t * E, t < T, r, E, p);  // on its way during the search
     const int s = b.seq_offsets ? find_sequence<LT>(b.seq_offsets, b.S, t) : 0;
     const bool live = t < T && s >= 0 && s < b.S && (!b.mask || b.mask[t] != 0);
-    float p[QQ], g[QQ];
-    load_token<LT, QQ>(logits + t * E, live, r, E, p);
-    token_softmax<LT, QQ>(live, r, E, p);
+    token_softmax<LT, QQ>(live, p);
     const float *co = b.coef + static_cast<int64_t>(live ? s : 0) * E;
     const float up = b.dloss ? *b.dloss : 1.0f;
     float c = 0.0f;
