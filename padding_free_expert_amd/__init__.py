@@ -178,7 +178,7 @@ _I32, _F32 = torch.int32, torch.float32
 def _shape(t: Optional[torch.Tensor], shape, name: str, dtype=None) -> None:
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, the call needs {dtype}")
