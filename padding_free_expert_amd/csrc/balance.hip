@@ -91,11 +91,10 @@ __device__ __forceinline__ void load_token(const float *row, bool live, int r, i
 }
 
 // Logits -> probabilities in place (dead tokens: 0).  exp(x - max) is taken as
-// 2^(x L - max L), L = log2(e), with one fused multiply-add: the rounding of
-// max L is the same factor in every term and leaves with the division, so the
-// error is that of the exponent's one rounding, |x - max| 2^-24, as with the
-// difference taken first.  (With expf and its range checks the arithmetic, not
-// the loads, bound these kernels: 44 vector instructions an element.)  One
+// 2^((x - max) L), L = log2(e): with expf and its range checks the arithmetic,
+// not the loads, bound these kernels (44 vector instructions an element).  The
+// difference comes first: x L - max L in one multiply-add saves an instruction,
+// but max L leaves fp32's range in a row of the type's lowest values.  One
 // division a token.
 template <int LT, int QQ>
 __device__ __forceinline__ void token_softmax(bool live, float (&p)[QQ]) {
@@ -105,11 +104,10 @@ __device__ __forceinline__ void token_softmax(bool live, float (&p)[QQ]) {
     for (int q = 0; q < QQ; ++q) mx = fmaxf(mx, p[q]);
 #pragma unroll
     for (int off = LT / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
-    const float shift = -mx * kLog2e;
     float den = 0.0f;
 #pragma unroll
     for (int q = 0; q < QQ; ++q) {  // 0 past E, where the logits are -infinity
-        p[q] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[q], kLog2e, shift));
+        p[q] = __builtin_amdgcn_exp2f((p[q] - mx) * kLog2e);
         den += p[q];
     }
 #pragma unroll

@@ -1,7 +1,9 @@
 """Balance loss, counts and gradient against the 64-bit definition.
 
-Bounds.  p: the argument of exp carries |s - max| 2^-24, at most 40 * 2^-24
-here, exp, the denominator and the division a few more: 2^-18 relative.  A
+Bounds.  p: the argument of exp carries |s - max| times 2.25 * 2^-24 (the
+difference, log2(e) in fp32 and the product), at most 24 times here (draws of
+1.5 normal + normal) or nothing of a p, exp, the denominator and the division
+ten halves more: 64 * 2^-24 = 2^-18 relative.  A
 sum of p has positive terms, at most 128 / 4 in sequence in a lane and a tree
 above it, then 64-bit sums: 2^-18 more.  coef is formed in 64 bits from
 alpha, rounded to fp32 by the call, and rounded once itself: (1 + 2^-24)^2 - 1,
@@ -132,6 +134,25 @@ def test_excluded_experts_and_odd_ids(xm):
     ids[0] = torch.tensor([7, 7, 7], device="cuda")
     ids[1] = torch.tensor([-1, E, 2], device="cuda")
     _check(xm, logits, ids, k, None, None)
+
+
+def test_rows_of_lowest_values(xm):
+    """Masks of the type's lowest value: a row with nothing else is uniform, and
+    large logits stay finite."""
+    big = torch.finfo(torch.float32).max
+    for T, E, k in ((40, 24, 3), (70, 33, 2), (64, 160, 8)):
+        logits, ids, _ = _case(T, E, k, seed=4)
+        logits[0] = -big
+        logits[1, 1:] = -big
+        logits[2] = big
+        logits[3, ::2] = -big
+        logits[4] = -big
+        logits[4, E - 1] = big
+        logits[5] += 1e9
+        logits[6] = -3e30
+        logits[7, : E // 2] = float("-inf")
+        logits[7, E // 2:] = -big
+        _check(xm, logits, ids, k, None, None, alpha=1.0)
 
 
 def test_gradient_against_differences(xm):
