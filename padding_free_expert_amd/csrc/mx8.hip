@@ -201,7 +201,6 @@ __device__ __forceinline__ bool wave_tile(const GemmArgs &p, int v, int tiles_n,
     const int base = __builtin_amdgcn_readfirstlane(static_cast<int>(lo));
     t->base = base;
     t->Mg = __builtin_amdgcn_readfirstlane(static_cast<int>(hi)) - base;
-    t->Kg = 0;
     return true;
 }
 
@@ -243,7 +242,7 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
         bsoff[j] = 4u * n;
     }
     // rows past the group's end read its first row and are not stored; ids outside
-    // the rows read row 0 and count as zeros
+    // the rows load zeros
     const uint8_t *const ab = p.map ? p.a : p.a + (t.base + t.m0) * K;
     const uint8_t *const as = p.map ? p.as : p.as + (t.base + t.m0) * 4;
     bool zero[MT];
@@ -272,23 +271,24 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
         const int64_t k = static_cast<int64_t>(s) * 128;
         const bool whole = k + 128 <= K;  // else K ends inside: elements past it are zeros
         const bool lo = whole || k + 16 * quad < K, hi = whole || k + 64 + 16 * quad < K;
-        auto load = [&](const uint8_t *q, uint32_t off) {
+        auto load = [&](const uint8_t *q, uint32_t off, bool none) {
             const i32x4_t z = {0, 0, 0, 0};
             const auto *a = reinterpret_cast<const i32x4_t *>(q + off);
-            const i32x4_t x = lo ? __builtin_nontemporal_load(a) : z, y = hi ? __builtin_nontemporal_load(a + 4) : z;
+            const i32x4_t x = lo && !none ? __builtin_nontemporal_load(a) : z;
+            const i32x4_t y = hi && !none ? __builtin_nontemporal_load(a + 4) : z;
             return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
         };
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int j = 0; j < NC; ++j) {
-                f.b[b][j] = load(wb[b] + k, boff[j]);
+                f.b[b][j] = load(wb[b] + k, boff[j], false);
                 f.bs[b][j] = *reinterpret_cast<const int *>(ws[b] + static_cast<int64_t>(s) * N * 4 + bsoff[j]);
             }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            f.a[i] = load(ab + k, aoff[i]);
-            f.as[i] = *reinterpret_cast<const int *>(as + static_cast<int64_t>(s) * p.a_rows * 4 + asoff[i]);
+            f.a[i] = load(ab + k, aoff[i], zero[i]);
+            f.as[i] = zero[i] ? 0 : *reinterpret_cast<const int *>(as + static_cast<int64_t>(s) * p.a_rows * 4 + asoff[i]);
         }
     };
     auto multiply = [&](const Step &f) {
@@ -322,9 +322,6 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
     const int m = t.m0 + 16 * mi + l16;
     const int64_t row = t.base + m;
     const bool live = m < t.Mg && c0 < N;
-    bool none = false;
-#pragma unroll
-    for (int i = 0; i < MT; ++i) none = i == mi ? zero[i] : none;
     f32x4_t v[NB][2];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -334,7 +331,6 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
             v[b][j] = part[0][f][lane];
 #pragma unroll
             for (int w = 1; w < KW; ++w) v[b][j] += part[w][f][lane];
-            if (none) v[b][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         }
     if constexpr (NB == 2) {
         float o[8];
@@ -527,8 +523,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             return find_tile<BM, BN>(tt, round * W + b % kXcds * kXcdRun + (b / kXcds + round) % kXcdRun, tiles_n);
         TileAt t = find_tile<BM, BN>(tt, split ? whole + (u - whole) / 2 : u, tiles_n);
         if (split) {
-            // a short tile's second half is empty: it starts at its end, never behind
-            // the rows, so that no buffer's size goes below zero
+            // a short tile's second half is empty and starts at its end
             const int from = min((u - whole) % 2 * WTM, t.rows);
             t.row += from;
             t.rows = min(t.rows - from, WTM);
@@ -555,8 +550,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     };
     auto source = [&](const TileAt &u) {
         Source q;
-        const int rows = u.rows, n0 = u.n0;
-        const int64_t r0 = u.row;
+        // An empty tile (half of a short one) loads the row in front of it: range
+        // checks take the scalar offset from the buffer's size, which for an empty
+        // buffer would leave what is below zero.
+        const int rows = max(u.rows, 1), n0 = u.n0;
+        const int64_t r0 = u.row - (u.rows > 0 ? 0 : 1);
         const int m = 64 * wave + lane;  // scales: wave w takes rows 64 w .. + 63 of A's 256 and of B's
         q.as_off = m < rows ? 4u * m : kOut;
         if constexpr (MAP) {

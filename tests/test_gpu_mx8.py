@@ -190,7 +190,10 @@ def _check_experts(xm, counts, d, h, T=None, seed=0, spare=0, tweak=None):
     ([129, 127, 128], 544, 128, 50), ([2, 1, 0, 1, 0, 0, 2, 1], 2048, 1408, 1), ([257, 511, 256, 0, 3], 384, 416, 700),
     ([1030, 70], 64, 640, 300), ([600, 900], 1024, 256, None),
     # row tiles whose second 128 rows are empty, at the end of the rows, with one 128-deep step
-    ([300, 260], 96, 128, None), ([300, 260], 128, 96, None), ([257, 1, 513], 64, 32, None), ([4, 900, 257], 128, 160, 90)])
+    ([300, 260], 96, 128, None), ([300, 260], 128, 96, None), ([257, 1, 513], 64, 32, None), ([4, 900, 257], 128, 160, 90),
+    # the most experts, for either kernel
+    ([i % 3 for i in range(1024)], 32, 64, 50), ([i % 29 for i in range(1023)] + [40], 64, 32, 700),
+    ([0] * 1000 + [600] + [0] * 22 + [300], 160, 96, None)])
 def test_experts(xm, counts, d, h, T):
     print(f"[experts8] counts={counts} d={d} h={h} T={T}", flush=True)
     _check_experts(xm, counts, d, h, T, seed=len(counts) + d)
@@ -225,6 +228,28 @@ def test_ids_outside_the_rows_read_zeros(xm):
         xm.xmoe_expert_ffn_up_mx8(xq, xs, w1, w1s, w3, w3s, off, act, acts, token_ids=ids)
         want[1] = want[3] = want[4] = 0
         assert torch.equal(br.mx8_values(act, acts), want)
+
+
+def test_weights_that_are_not_finite(xm):
+    """A NaN in a weight makes NaNs of what reads it, a row of zeros included, and
+    of nothing else, in either kernel."""
+    for c in (4, 300):
+        d, h = 160, 96
+        w1, w1s, w3, w3s, w2, w2s = _experts(xm, 3, d, h, 5)
+        w1s[1, 0, 40, 2] = 255        # expert 1, column 40, elements 64 .. 95
+        xq, xs = _quantize(xm, torch.randn((c, d), generator=_gen(1), device="cuda").to(BF))
+        ids = torch.arange(3 * c, dtype=torch.int32, device="cuda") % c
+        ids[0] = ids[c] = ids[c + 2] = -1
+        off = torch.tensor([0, c, 2 * c, 3 * c], dtype=torch.int32, device="cuda")
+        act, acts = (torch.empty((3 * c, h), dtype=F8, device="cuda"),
+                     torch.empty(xm.mx8_scale_shape(3 * c, h), dtype=U8, device="cuda"))
+        xm.xmoe_expert_ffn_up_mx8(xq, xs, w1, w1s, w3, w3s, off, act, acts, token_ids=ids)
+        v = br.mx8_values(act, acts)
+        bad = torch.isnan(v)
+        want = torch.zeros_like(bad)
+        want[c: 2 * c, 32:64] = True  # the block of 32 that holds the column
+        assert torch.equal(bad, want)
+        assert bool((v[0] == 0).all()) and bool((v[c][:32] == 0).all())
 
 
 def test_no_rows(xm):
