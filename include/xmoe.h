@@ -508,7 +508,9 @@ xmoe_status xmoe_scatter_rows(const void *src, xmoe_dtype dtype, int64_t n, int3
  * may be NULL; y, q or both are required.  q (e4m3 [T,d]) with scale is y in 8
  * bits (see xmoe_mx8_quantize), quantized from the fp32 values: one rounding.
  * sum or y may be the buffer of x or of res.  Each row is read and written
- * once.  Non-finite inputs: an infinity or a NaN in a row makes NaNs of its y.
+ * once.  Squares are summed in fp32: a NaN makes NaNs of its row's y; an infinity
+ * one in its own place and zeros elsewhere (rstd = 0), and so, without the NaN,
+ * do finite values whose squares leave fp32's range (past 2^63).
  * Limits: d % 8 == 0 (q: % 32 == 0), d <= 16384, T * max(d, 512) < 2^34,
  * eps >= 0.
  */
@@ -595,7 +597,7 @@ xmoe_status xmoe_route_bwd_balance(const void *x, const void *wg, const float *l
  *   xmoe_mx8_quantize_weights: w [E,K,N] (dtype, the layer's layout) -> q
  *                        [E,N,K], scale [E, ceil(K/128), N, 4], the summed axis
  *                        last; once per weight update.
- * Limits: K (and N) multiples of 32, at most 65536; n * max(K, 512) < 2^34;
+ * Limits: K (and N) multiples of 32, at most 65536; n * max(K, 512) < 2^33;
  * E <= 1024, E * ceil(K/128) * ceil(N/64) < 2^24.  All arrays 16-byte aligned.
  */
 xmoe_status xmoe_mx8_quantize(const void *x, xmoe_dtype dtype, int64_t n, int32_t K, void *q, void *scale,
@@ -610,7 +612,11 @@ xmoe_status xmoe_mx8_quantize_weights(const void *w, xmoe_dtype dtype, int32_t E
  *   up   : H1 = x[r] . w1[e], H3 = x[r] . w3[e];  act[r] = silu(H1) * H3 in 8 bits
  *   down : ye[r] = act[r] . w2[e]                          (bf16 [rows,d])
  * for the rows r of expert e, the products of the values that the 8-bit
- * operands stand for, summed in fp32; act is quantized from fp32.
+ * operands stand for, summed in fp32; act is quantized from fp32.  The matrix
+ * instruction adds eight products at a time, each cut at 2^-13 of the power of
+ * two of the largest: a sum is within (2^-10 + K 2^-24) of the sum of its
+ * products' magnitudes, in practice 2^-14 of itself, so that an element of act
+ * next to a rounding boundary may be the neighbouring value.
  * xq, xscale: 8-bit rows [T,d]; row r of the experts' rows is row token_ids[r]
  * of them (DEVICE int32 [rows]; ids outside [0,T) read a row of zeros), or row
  * r itself with token_ids NULL (then T == rows).  w1, w3 [E,h,d] and w2 [E,d,h]

@@ -12,7 +12,8 @@ using namespace xmoe_api;
 
 namespace {
 
-constexpr int64_t kMaxElems = int64_t(1) << 34;  // rows * max(d, 512): the launch's threads stay below 2^32
+constexpr int64_t kMaxElems = int64_t(1) << 34;     // rows * max(d, 512): the launch's threads stay below 2^32
+constexpr int64_t kMaxMx8Elems = int64_t(1) << 33;  // the same for fp32 rows in whole waves (544: 192 threads a row)
 constexpr int32_t kMaxNormDim = 16384;
 constexpr int32_t kMaxMx8Dim = 65536;
 constexpr int64_t kMaxBalanceTokens = int64_t(1) << 26;
@@ -47,7 +48,7 @@ xmoe_status check_mx8_rows(int64_t n, int32_t K) {
     REQUIRE(n >= 0 && K >= 1, XMOE_ERR_INVALID_VALUE, "n must be >= 0 and K >= 1");
     REQUIRE(K % 32 == 0, XMOE_ERR_UNSUPPORTED, "K must be a multiple of 32");
     REQUIRE(K <= kMaxMx8Dim, XMOE_ERR_UNSUPPORTED, "K must be at most %d", kMaxMx8Dim);
-    REQUIRE(within(n, std::max(K, 512), kMaxElems - 1), XMOE_ERR_INVALID_VALUE, "n * max(K, 512) must be < 2^34");
+    REQUIRE(within(n, std::max(K, 512), kMaxMx8Elems - 1), XMOE_ERR_INVALID_VALUE, "n * max(K, 512) must be < 2^33");
     return XMOE_OK;
 }
 
@@ -83,6 +84,8 @@ xmoe_status xmoe_add_rmsnorm(const void *x, const void *res, const void *gamma, 
         REQUIRE(same_or_apart(o, x, bytes) && same_or_apart(o, res, bytes), XMOE_ERR_INVALID_VALUE,
                 "sum and y may be x or res, but not overlap them otherwise");
     REQUIRE(!overlap(sum, bytes, y, bytes), XMOE_ERR_INVALID_VALUE, "sum and y must not overlap");
+    for (const void *o : {x, res, static_cast<const void *>(sum), static_cast<const void *>(y)})
+        REQUIRE(!overlap(q, T * d, o, bytes), XMOE_ERR_INVALID_VALUE, "q must not overlap x, res, sum or y");
     CHECK_DEVICE();
     return hip_status(xmoe::launch_add_rmsnorm(dtype, x, res, gamma, T, d, eps, sum, y, q, scale, rstd, S(stream)),
                       "xmoe_add_rmsnorm launch");
@@ -185,6 +188,8 @@ xmoe_status xmoe_mx8_quantize(const void *x, xmoe_dtype dtype, int64_t n, int32_
     TRY(check_mx8_rows(n, K));
     REQUIRE(n == 0 || (x && q && scale), XMOE_ERR_INVALID_VALUE, "x, q and scale are required");
     REQUIRE(aligned16(x) && aligned16(q) && aligned16(scale), XMOE_ERR_UNSUPPORTED, "matrices must be 16-byte aligned");
+    REQUIRE(!overlap(q, n * K, x, n * K * (dtype == XMOE_BF16 ? 2 : 4)), XMOE_ERR_INVALID_VALUE,
+            "q must not overlap x");
     CHECK_DEVICE();
     return hip_status(xmoe::launch_mx8_quantize(dtype, x, n, K, q, scale, S(stream)), "xmoe_mx8_quantize launch");
 }

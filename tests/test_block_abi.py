@@ -40,6 +40,8 @@ def test_norm_rejects_on_host(xm):
     assert f(y=_at(16)) == INVALID                    # overlaps x in part
     assert f(res=_at(1 << 17), sum=_at((1 << 17) + 32)) == INVALID
     assert f(sum=_at(1 << 16)) == INVALID             # sum and y
+    assert f(q=P, scale=_at(1 << 18)) == INVALID      # q and x
+    assert f(q=_at((1 << 16) + 64), scale=_at(1 << 18)) == INVALID   # q and y
     # in place is allowed: what follows is the device check
     assert f(y=P) not in (INVALID, UNSUPPORTED, WORKSPACE)
     assert f(res=_at(1 << 17), sum=_at(1 << 17)) not in (INVALID, UNSUPPORTED, WORKSPACE)
@@ -100,6 +102,8 @@ def test_mx8_rejects_on_host(xm):
     assert q(None, 1, 10, 64, P, P, None) == INVALID and q(P, 1, -1, 64, P, P, None) == INVALID
     assert q(P, 1, 1 << 25, 64, P, P, None) == INVALID and q(P, 3, 10, 64, P, P, None) == UNSUPPORTED
     assert q(ODD, 1, 10, 64, P, P, None) == UNSUPPORTED
+    assert q(_at(1 << 16), 0, 1 << 24, 544, P, P, None) == INVALID   # n * max(K, 512) >= 2^33
+    assert q(P, 1, 10, 64, _at(640), P, None) == INVALID             # q and x
     dq = xm._lib_mx8_dq
     assert dq(P, None, 1, 10, 64, P, None) == INVALID and dq(P, P, 1, 10, 63, P, None) == UNSUPPORTED
     qw = xm._lib_mx8_qw
