@@ -14,8 +14,11 @@
 // sequences both only go forward, so no two pieces share a row and the rows
 // number at most chunks + S.  A second kernel adds a sequence's rows in order and
 // writes counts and coef; its last block to end adds the blocks' losses in
-// order.  Nothing depends on the order in which blocks run.  Memory-bound: the
-// logits are read once here, once in the backward, which writes the gradient.
+// order.  Nothing depends on the order in which blocks run.  The logits are read
+// once here, once in the backward, which writes the gradient.  Bound by latency:
+// 4096 tokens of 64 experts take 3.7 + 6.2 us and 3.4 us back, most of it launch,
+// first loads and the hand-over between compute units; 32768 of 160 experts in
+// 24 sequences (63 MB in all) 11.2 + 7.2 and 10.1 us.
 #include <algorithm>
 
 #include "balance.hpp"
@@ -28,11 +31,15 @@ namespace {
 
 constexpr int kWaves = 4;
 
-// Tokens per block: about 2048 blocks, eight on each compute unit, at least one
-// step of every wave; at most 128, so that a sum of p has few terms in sequence
+// Tokens per block: about 512 blocks, two on each compute unit, at least one
+// step of every wave; at most 128, so that a sum of p has few terms in sequence.
+// More and smaller blocks leave the second kernel more rows: against 2048 blocks
+// 16384 tokens of 64 experts 11.1 and 12.9 us (both kernels), 32768 of 160 in 24
+// sequences 17.6 and 19.3, 131072 of 64 19.3 and 23.2; 65536 of 64 in 8
+// sequences 15.6 and 15.0.
 inline int chunk_tokens(int64_t T) {
     int c = 16;
-    while (c < 128 && T > static_cast<int64_t>(c) * 2048) c *= 2;
+    while (c < 128 && T > static_cast<int64_t>(c) * 512) c *= 2;
     return c;
 }
 // experts per block of the second kernel: its 32 row groups share a sequence's rows
@@ -375,7 +382,9 @@ __global__ __launch_bounds__(64 * kWaves) void balance_bwd_kernel(const float *_
     }
 }
 
-// Lanes per token and experts per lane: at most 16 experts a lane up to 512
+// Lanes per token and experts per lane: at most 16 experts a lane up to 512.
+// Forward, 32768 tokens of 160 experts, both kernels: 16 lanes 21.4 us, 8 lanes
+// 26.6, 32 lanes 22.2 (one sequence).
 #define XMOE_BALANCE_SHAPE(E, CALL)      \
     do {                                 \
         if ((E) <= 32) CALL(8, 4);       \
@@ -386,6 +395,13 @@ __global__ __launch_bounds__(64 * kWaves) void balance_bwd_kernel(const float *_
         else if ((E) <= 512) CALL(32, 16); \
         else CALL(32, 32);               \
     } while (0)
+// With many tokens 8 lanes a token, fewer steps between lanes.  Backward, up to
+// 256 experts (32768 tokens of 64, 160, 256 experts 5.2, 9.5, 14.8 us against 6.0,
+// 11.2, 16.7; 16384 of 160 6.6 against 7.0; 8192 of 160 5.2 against 4.9; 32768 of
+// 512 29.3 against 28.0); forward, up to 128, whose lanes hold the sums too (32768
+// tokens of 64 and 128 11.6 and 13.4 us against 12.9 and 13.7; 131072 of 64 17.5
+// against 19.8, of 160 in 64 sequences 30.3 against 29.9).
+constexpr int64_t kManyTokens = 16384;
 
 }  // namespace
 
@@ -401,7 +417,10 @@ hipError_t launch_balance_loss(const float *logits, const int32_t *ids, int64_t 
 #define XMOE_BALANCE_PART(LT, QQ)                                                                                  \
     hipLaunchKernelGGL((balance_part_kernel<LT, QQ>), dim3(blocks), dim3(64 * kWaves), 0, st, logits, ids, T, E, k, \
                        seq_offsets, S, mask, chunk, w)
-    XMOE_BALANCE_SHAPE(E, XMOE_BALANCE_PART);
+    const bool many = T >= kManyTokens && E > 32;
+    if (many && E <= 64) XMOE_BALANCE_PART(8, 8);
+    else if (many && E <= 128) XMOE_BALANCE_PART(8, 16);
+    else XMOE_BALANCE_SHAPE(E, XMOE_BALANCE_PART);
 #undef XMOE_BALANCE_PART
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -417,7 +436,12 @@ hipError_t launch_balance_loss_bwd(const float *logits, int64_t T, int E, const 
     hipLaunchKernelGGL((balance_bwd_kernel<LT, QQ>),                                                                 \
                        dim3(static_cast<unsigned>((T + kWaves * (64 / (LT)) - 1) / (kWaves * (64 / (LT))))),         \
                        dim3(64 * kWaves), 0, st, logits, T, E, b, dlogits)
-    XMOE_BALANCE_SHAPE(E, XMOE_BALANCE_BWD);
+    const bool many = T >= kManyTokens && E > 32;
+    if (many && E <= 64) XMOE_BALANCE_BWD(8, 8);
+    else if (many && E <= 128) XMOE_BALANCE_BWD(8, 16);
+    else if (many && E <= 192) XMOE_BALANCE_BWD(8, 24);
+    else if (many && E <= 256) XMOE_BALANCE_BWD(8, 32);
+    else XMOE_BALANCE_SHAPE(E, XMOE_BALANCE_BWD);
 #undef XMOE_BALANCE_BWD
     return hipGetLastError();
 }

@@ -65,7 +65,8 @@ def _check(xm, logits, ids, k, off, mask, alpha=0.01, up=None):
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (15, 8, 8), (16, 64, 6), (17, 33, 3), (100, 100, 5), (512, 160, 8),
                                    (1000, 129, 1), (4096, 64, 6), (8193, 256, 8), (70000, 24, 2), (300, 513, 7),
-                                   (257, 1024, 64), (33, 1021, 8)])
+                                   (257, 1024, 64), (33, 1021, 8), (16391, 50, 3), (16384, 97, 2), (20001, 192, 8),
+                                   (16399, 250, 4)])
 def test_one_sequence(xm, T, E, k):
     print(f"[balance] T={T} E={E} k={k}", flush=True)
     logits, ids, g = _case(T, E, k, seed=T + E)
@@ -77,7 +78,7 @@ def test_one_sequence(xm, T, E, k):
 @pytest.mark.parametrize("T,E,k,off", [
     (40, 16, 2, [0, 40]), (40, 16, 2, [0, 0, 40, 40]), (40, 16, 2, [3, 10, 10, 10, 33]),
     (300, 64, 6, [0, 16, 32, 33, 300]), (1000, 40, 4, [0, 1, 2, 3, 900, 901, 1000]),
-    (2000, 160, 8, [100, 100]), (129, 512, 3, [0, 128, 129])])
+    (2000, 160, 8, [100, 100]), (129, 512, 3, [0, 128, 129]), (17000, 72, 6, [5, 9000, 9000, 16003, 16999])])
 def test_sequences(xm, T, E, k, off):
     print(f"[balance] T={T} E={E} off={off}", flush=True)
     logits, ids, g = _case(T, E, k, seed=T)
