@@ -191,6 +191,9 @@ def _check_experts(xm, counts, d, h, T=None, seed=0, spare=0, tweak=None):
     ([1030, 70], 64, 640, 300), ([600, 900], 1024, 256, None),
     # row tiles whose second 128 rows are empty, at the end of the rows, with one 128-deep step
     ([300, 260], 96, 128, None), ([300, 260], 128, 96, None), ([257, 1, 513], 64, 32, None), ([4, 900, 257], 128, 160, 90),
+    # last row tiles of every height
+    ([256 + r for r in (1, 31, 64, 127, 128, 129, 160, 191, 192, 193, 224, 255)], 288, 160, 300),
+    ([r for r in (129, 192, 193, 160, 256, 191, 130)], 160, 352, None),
     # the most experts, for either kernel
     ([i % 3 for i in range(1024)], 32, 64, 50), ([i % 29 for i in range(1023)] + [40], 64, 32, 700),
     ([0] * 1000 + [600] + [0] * 22 + [300], 160, 96, None)])
