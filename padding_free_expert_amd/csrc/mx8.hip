@@ -216,20 +216,19 @@ __device__ __forceinline__ bool wave_tile(const GemmArgs &p, int v, int tiles_n,
 // Few rows per expert: the weights are streamed past the rows once.  A block
 // takes 16 MT rows of one expert by 64 weight rows (32 of W1 and the same of W3
 // for the up-projection, NB = 2) and its four waves split the summed axis in
-// 128-deep steps; operands go from memory straight to registers, since no other
-// wave of the block needs them.  The waves' partial sums meet in LDS, added in
-// wave order.  Bound by the weights' bytes: what counts is loads in flight, so
-// registers are kept few enough for five blocks on a compute unit rather than
-// spent on a second step's loads (96 tokens, 64 experts of d = 2048, h = 1408,
-// top-6, up and down: 123 + 77 us in that form, 86 + 45 in this).  Kernel times
-// there 78 + 44 us, 4.7 and 4.2 TB/s of weights; one token 16 + 9 us, where 264
-// and 192 blocks on 256 compute units each wait for cold memory.
+// 128-deep steps.  The waves' partial sums meet in LDS, added in wave order.
+// Bound by the weights' bytes: what counts is whole lines in flight, so weights
+// come as lines through a piece of shared memory of each wave's own (with loads in
+// the instruction's order, 96 tokens of 64 experts of d = 2048, h = 1408, top-6
+// took 78 + 44 us up and down, now 60 + 33: 6.2 and 5.6 TB/s), and registers are
+// kept few enough for four blocks on a compute unit.  One token 11.7 + 8.6 us, of
+// which 3.7 and 3.0 are launch and the tile's search.
 template <int NB, int MT>
 __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
     constexpr int KW = 4, NC = 4 / NB, BM = 16 * MT, BN = 16 * NC;
     constexpr int NF = 4 * MT;  // 16 x 16 results of a wave
     __shared__ f32x4_t part[KW][NF][64];
-    static_assert(sizeof(part) <= 32 * 1024, "five blocks on a compute unit");
+    static_assert(sizeof(part) <= 32 * 1024, "four blocks on a compute unit");
     static_assert(KW >= MT * (NB == 1 ? 2 : 1), "a wave for each 16 rows (and 32 columns) of the result");
     const int N = p.g.N, K = p.K, kb = (K + 127) / 128;
     Tile t;
@@ -239,20 +238,22 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
     const int l16 = lane & 15, quad = lane >> 4;
     const int n0 = t.nt * BN;
 
-    // offsets of this lane's rows from uniform bases that move with k
+    // Weights come as whole 128-byte lines, eight rows a load (lane l: chunk l % 8 of
+    // row l / 8, then of row 8 + l / 8), and go through a piece of shared memory of
+    // the wave's own into the order of the instruction, whose 16 neighbouring lanes
+    // hold 16 rows: asked for in that order, a load would touch 16 lines for 16 bytes
+    // each.  Uniform bases that move with k; columns past N read the tile's first.
     const uint8_t *wb[2], *ws[2];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         wb[b] = (b ? p.b1 : p.b0) + (static_cast<int64_t>(t.g) * N + n0) * K;
         ws[b] = (b ? p.b1s : p.b0s) + (static_cast<int64_t>(t.g) * kb * N + n0) * 4;
     }
-    uint32_t boff[NC], bsoff[NC], aoff[MT], asoff[MT];
+    uint32_t aoff[MT], asoff[MT];
+    const uint32_t boff = static_cast<uint32_t>(lane >> 3) * static_cast<uint32_t>(K) + 16 * (lane & 7);
+    int col[NC];
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-        const int n = min(16 * j + l16, N - 1 - n0);  // past N: a row again, not stored
-        boff[j] = static_cast<uint32_t>(n) * static_cast<uint32_t>(K) + 16 * quad;
-        bsoff[j] = 4u * n;
-    }
+    for (int j = 0; j < NC; ++j) col[j] = n0 + 16 * j < N ? 16 * j : 0;
     // rows past the group's end read its first row and are not stored; ids outside
     // the rows load zeros
     const uint8_t *const ab = p.map ? p.a : p.a + (t.base + t.m0) * K;
@@ -276,13 +277,19 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
             for (int i = 0; i < MT; ++i) acc[b][j][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
     struct Step {
-        i32x8_t b[NB][NC], a[MT];
+        i32x4_t b[NB][NC][2];
+        i32x8_t a[MT];
         int bs[NB][NC], as[MT];
     };
     auto fetch = [&](int s, Step &f) {
         const int64_t k = static_cast<int64_t>(s) * 128;
         const bool whole = k + 128 <= K;  // else K ends inside: elements past it are zeros
         const bool lo = whole || k + 16 * quad < K, hi = whole || k + 64 + 16 * quad < K;
+        const bool in = whole || k + 16 * (lane & 7) < K;
+        auto line = [&](const uint8_t *q) {
+            const i32x4_t z = {0, 0, 0, 0};
+            return in ? __builtin_nontemporal_load(reinterpret_cast<const i32x4_t *>(q + boff)) : z;
+        };
         auto load = [&](const uint8_t *q, uint32_t off, bool none) {
             const i32x4_t z = {0, 0, 0, 0};
             const auto *a = reinterpret_cast<const i32x4_t *>(q + off);
@@ -294,8 +301,10 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int j = 0; j < NC; ++j) {
-                f.b[b][j] = load(wb[b] + k, boff[j], false);
-                f.bs[b][j] = *reinterpret_cast<const int *>(ws[b] + static_cast<int64_t>(s) * N * 4 + bsoff[j]);
+                const uint8_t *const q = wb[b] + static_cast<int64_t>(col[j]) * K + k;
+                f.b[b][j][0] = line(q);
+                f.b[b][j][1] = line(q + 8 * static_cast<int64_t>(K));
+                f.bs[b][j] = *reinterpret_cast<const int *>(ws[b] + (static_cast<int64_t>(s) * N + col[j]) * 4 + 4 * l16);
             }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
@@ -303,15 +312,31 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
             f.as[i] = zero[i] ? 0 : *reinterpret_cast<const int *>(as + static_cast<int64_t>(s) * p.a_rows * 4 + asoff[i]);
         }
     };
+    // two slots of 2 KB in the wave's part of `part`, chunk c of row r at c ^ (r % 8)
+    char *const stage = reinterpret_cast<char *>(&part[wave][0][0]);
+    static_assert(NF * 64 * sizeof(f32x4_t) >= 4096, "two slots");
+    char *const put = stage + (lane >> 3) * 128 + 16 * ((lane & 7) ^ (lane >> 3));
+    const char *const lo_at = stage + l16 * 128 + 16 * (quad ^ (l16 & 7));
+    const char *const hi_at = stage + l16 * 128 + 16 * ((4 + quad) ^ (l16 & 7));
     auto multiply = [&](const Step &f) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int j = 0; j < NC; ++j)
+            for (int j = 0; j < NC; ++j) {
+                const int at = ((b * NC + j) & 1) * 2048;
+                *reinterpret_cast<i32x4_t *>(put + at) = f.b[b][j][0];
+                *reinterpret_cast<i32x4_t *>(put + at + 1024) = f.b[b][j][1];
+                // a wave's accesses to shared memory are served in order
+                __builtin_amdgcn_wave_barrier();
+                const i32x4_t lo = *reinterpret_cast<const i32x4_t *>(lo_at + at);
+                const i32x4_t hi = *reinterpret_cast<const i32x4_t *>(hi_at + at);
+                __builtin_amdgcn_wave_barrier();
+                const i32x8_t w = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
                     acc[b][j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        f.b[b][j], f.a[i], acc[b][j][i], 0, 0, 0, f.bs[b][j] >> (8 * quad), 0, f.as[i] >> (8 * quad));
+                        w, f.a[i], acc[b][j][i], 0, 0, 0, f.bs[b][j] >> (8 * quad), 0, f.as[i] >> (8 * quad));
+            }
     };
 #pragma unroll 1
     for (int s = wave; s < kb; s += KW) {
