@@ -217,12 +217,14 @@ __device__ __forceinline__ bool wave_tile(const GemmArgs &p, int v, int tiles_n,
 // takes 16 MT rows of one expert by 64 weight rows (32 of W1 and the same of W3
 // for the up-projection, NB = 2) and its four waves split the summed axis in
 // 128-deep steps.  The waves' partial sums meet in LDS, added in wave order.
-// Bound by the weights' bytes: what counts is whole lines in flight, so weights
+// Bound by the weights' bytes: what counts is whole lines in flight, so operands
 // come as lines through a piece of shared memory of each wave's own (with loads in
 // the instruction's order, 96 tokens of 64 experts of d = 2048, h = 1408, top-6
 // took 78 + 44 us up and down, now 60 + 33: 6.2 and 5.6 TB/s), and registers are
-// kept few enough for four blocks on a compute unit.  One token 11.7 + 8.6 us, of
-// which 3.7 and 3.0 are launch and the tile's search.
+// kept few enough for four blocks on a compute unit (eight waves a block 65 + 38, a
+// second step's loads ahead 65 + 38).  Weights are loaded past the caches (else 67
+// + 38), rows are not (4 experts of 64 rows 13.9 + 11.1 against 16.1 + 12.3 us).  One
+// token 11.5 + 8.1 us, of which 3.7 and 3.0 are launch and the tile's search.
 template <int NB, int MT>
 __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
     constexpr int KW = 4, NC = 4 / NB, BM = 16 * MT, BN = 16 * NC;
@@ -238,7 +240,7 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
     const int l16 = lane & 15, quad = lane >> 4;
     const int n0 = t.nt * BN;
 
-    // Weights come as whole 128-byte lines, eight rows a load (lane l: chunk l % 8 of
+    // Operands come as whole 128-byte lines, eight rows a load (lane l: chunk l % 8 of
     // row l / 8, then of row 8 + l / 8), and go through a piece of shared memory of
     // the wave's own into the order of the instruction, whose 16 neighbouring lanes
     // hold 16 rows: asked for in that order, a load would touch 16 lines for 16 bytes
@@ -249,7 +251,7 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
         wb[b] = (b ? p.b1 : p.b0) + (static_cast<int64_t>(t.g) * N + n0) * K;
         ws[b] = (b ? p.b1s : p.b0s) + (static_cast<int64_t>(t.g) * kb * N + n0) * 4;
     }
-    uint32_t aoff[MT], asoff[MT];
+    uint32_t aoff[MT][2], asoff[MT];
     const uint32_t boff = static_cast<uint32_t>(lane >> 3) * static_cast<uint32_t>(K) + 16 * (lane & 7);
     int col[NC];
 #pragma unroll
@@ -258,15 +260,19 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
     // the rows load zeros
     const uint8_t *const ab = p.map ? p.a : p.a + (t.base + t.m0) * K;
     const uint8_t *const as = p.map ? p.as : p.as + (t.base + t.m0) * 4;
-    bool zero[MT];
+    bool zero[MT][2], szero[MT];
+    auto row_of = [&](int r, bool *none) {
+        const int m = t.m0 + r < t.Mg ? r : 0;
+        const int id = p.map ? p.map[t.base + t.m0 + m] : m;
+        *none = p.map && (id < 0 || id >= p.a_rows);
+        return *none ? 0u : static_cast<uint32_t>(id);
+    };
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const int m = t.m0 + 16 * i + l16 < t.Mg ? 16 * i + l16 : 0;
-        int id = p.map ? p.map[t.base + t.m0 + m] : m;
-        zero[i] = p.map && (id < 0 || id >= p.a_rows);
-        if (zero[i]) id = 0;
-        aoff[i] = static_cast<uint32_t>(id) * static_cast<uint32_t>(K) + 16 * quad;
-        asoff[i] = 4u * id;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+            aoff[i][y] = row_of(16 * i + 8 * y + (lane >> 3), &zero[i][y]) * static_cast<uint32_t>(K) + 16 * (lane & 7);
+        asoff[i] = 4u * row_of(16 * i + l16, &szero[i]);
     }
     f32x4_t acc[NB][NC][MT];
 #pragma unroll
@@ -278,25 +284,26 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
 
     struct Step {
         i32x4_t b[NB][NC][2];
-        i32x8_t a[MT];
+        i32x4_t a[MT][2];
         int bs[NB][NC], as[MT];
     };
     auto fetch = [&](int s, Step &f) {
         const int64_t k = static_cast<int64_t>(s) * 128;
         const bool whole = k + 128 <= K;  // else K ends inside: elements past it are zeros
-        const bool lo = whole || k + 16 * quad < K, hi = whole || k + 64 + 16 * quad < K;
         const bool in = whole || k + 16 * (lane & 7) < K;
         auto line = [&](const uint8_t *q) {
             const i32x4_t z = {0, 0, 0, 0};
             return in ? __builtin_nontemporal_load(reinterpret_cast<const i32x4_t *>(q + boff)) : z;
         };
-        auto load = [&](const uint8_t *q, uint32_t off, bool none) {
-            const i32x4_t z = {0, 0, 0, 0};
-            const auto *a = reinterpret_cast<const i32x4_t *>(q + off);
-            const i32x4_t x = lo && !none ? __builtin_nontemporal_load(a) : z;
-            const i32x4_t y = hi && !none ? __builtin_nontemporal_load(a + 4) : z;
-            return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-        };
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const i32x4_t z = {0, 0, 0, 0};
+                f.a[i][y] = in && !zero[i][y] ? *reinterpret_cast<const i32x4_t *>(ab + k + aoff[i][y]) : z;
+            }
+            f.as[i] = szero[i] ? 0 : *reinterpret_cast<const int *>(as + static_cast<int64_t>(s) * p.a_rows * 4 + asoff[i]);
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -306,11 +313,6 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
                 f.b[b][j][1] = line(q + 8 * static_cast<int64_t>(K));
                 f.bs[b][j] = *reinterpret_cast<const int *>(ws[b] + (static_cast<int64_t>(s) * N + col[j]) * 4 + 4 * l16);
             }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            f.a[i] = load(ab + k, aoff[i], zero[i]);
-            f.as[i] = zero[i] ? 0 : *reinterpret_cast<const int *>(as + static_cast<int64_t>(s) * p.a_rows * 4 + asoff[i]);
-        }
     };
     // two slots of 2 KB in the wave's part of `part`, chunk c of row r at c ^ (r % 8)
     char *const stage = reinterpret_cast<char *>(&part[wave][0][0]);
@@ -318,24 +320,29 @@ __global__ __launch_bounds__(256) void mx8_stream_kernel(Mx8Args p) {
     char *const put = stage + (lane >> 3) * 128 + 16 * ((lane & 7) ^ (lane >> 3));
     const char *const lo_at = stage + l16 * 128 + 16 * (quad ^ (l16 & 7));
     const char *const hi_at = stage + l16 * 128 + 16 * ((4 + quad) ^ (l16 & 7));
+    auto turn = [&](const i32x4_t (&v)[2], int at) {
+        *reinterpret_cast<i32x4_t *>(put + at) = v[0];
+        *reinterpret_cast<i32x4_t *>(put + at + 1024) = v[1];
+        // a wave's accesses to shared memory are served in order
+        __builtin_amdgcn_wave_barrier();
+        const i32x4_t lo = *reinterpret_cast<const i32x4_t *>(lo_at + at);
+        const i32x4_t hi = *reinterpret_cast<const i32x4_t *>(hi_at + at);
+        __builtin_amdgcn_wave_barrier();
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
     auto multiply = [&](const Step &f) {
+        i32x8_t a[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) a[i] = turn(f.a[i], (i & 1) * 2048);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int j = 0; j < NC; ++j) {
-                const int at = ((b * NC + j) & 1) * 2048;
-                *reinterpret_cast<i32x4_t *>(put + at) = f.b[b][j][0];
-                *reinterpret_cast<i32x4_t *>(put + at + 1024) = f.b[b][j][1];
-                // a wave's accesses to shared memory are served in order
-                __builtin_amdgcn_wave_barrier();
-                const i32x4_t lo = *reinterpret_cast<const i32x4_t *>(lo_at + at);
-                const i32x4_t hi = *reinterpret_cast<const i32x4_t *>(hi_at + at);
-                __builtin_amdgcn_wave_barrier();
-                const i32x8_t w = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                const i32x8_t w = turn(f.b[b][j], ((b * NC + j) & 1) * 2048);
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
                     acc[b][j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        w, f.a[i], acc[b][j][i], 0, 0, 0, f.bs[b][j] >> (8 * quad), 0, f.as[i] >> (8 * quad));
+                        w, a[i], acc[b][j][i], 0, 0, 0, f.bs[b][j] >> (8 * quad), 0, f.as[i] >> (8 * quad));
             }
     };
 #pragma unroll 1
@@ -946,16 +953,19 @@ Mx8Args rows_args(const int32_t *offsets, int E, int64_t rows, int N, int K) {
 
 template <int NB>
 hipError_t product(const Mx8Args &p, hipStream_t s) {
-    // Up to 10 rows per expert the stream kernel reads the weights faster (9 rows
-    // on 64 experts of d = 2048, h = 1408, up and down: 86 + 45 us against the tile
-    // kernel's 98 + 46; 12 rows: 100 + 51 against 98 + 46).  Where the tile kernel
-    // has no tile for every compute unit, the stream kernel's 32-row form, whose
-    // tiles are 64 columns narrow, is ahead up to 64 rows (4 experts of 64 rows: 29
-    // + 17 against 37 + 21 us; of 128 rows: 41 + 22 against 37 + 21).
+    // Up + down, 64 experts of d = 2048, h = 1408: the stream kernel with 16 rows a
+    // block, with 32, and the tile kernel take at 9 rows an expert 60 + 33, 63 + 33
+    // and 80 + 43 us; at 12 63 + 35, 64 + 33 and 80 + 44; at 16 75 + 41, 65 + 35 and
+    // 81 + 44; at 28 100 + 56, 79 + 43 and 81 + 46; at 40 128 + 69, 116 + 63 and 82 +
+    // 47.  With more rows each 32 of them read the weights again, which pays only
+    // where the launch is so small that the tile kernel leaves compute units idle:
+    // three stream blocks for each unit at most (4 such experts of 64, 96 and 128
+    // rows 13 + 10, 17 + 10 and 23 + 14 us, tiles 21 + 16; 16 experts of d = 512, h =
+    // 256 with 128 and 500 rows 8 + 6 and 21 + 15, tiles 12 + 9 and 13 + 10).
     const int64_t rows = p.g.extent, active = std::min<int64_t>(p.g.G, rows);
-    const int64_t tiles = (rows / 256 + active) * ((p.g.N + 256 / NB - 1) / (256 / NB));
-    if (rows <= 10 * active) return launch_stream<NB, 1>(p, s);
-    if (tiles < kComputeUnits && rows <= 64 * active) return launch_stream<NB, 2>(p, s);
+    const int64_t blocks = (rows / 32 + active) * ((p.g.N + 64 / NB - 1) / (64 / NB));
+    if (rows <= 12 * active) return launch_stream<NB, 1>(p, s);
+    if (rows <= 28 * active || blocks <= 3 * kComputeUnits) return launch_stream<NB, 2>(p, s);
     if constexpr (NB == 2) {
         if (p.map) return launch_tile<2, true>(p, s);
     }
