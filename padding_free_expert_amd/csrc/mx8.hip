@@ -415,12 +415,20 @@ __device__ __forceinline__ uint32_t fresh(uint32_t v) {
     return v;
 }
 
-// direct-to-LDS loads as those of gemm.hpp, with a scalar offset
+// direct-to-LDS loads as those of gemm.hpp, with a scalar offset; NT: past the
+// caches
+template <bool NT = false>
 __device__ __forceinline__ void lds_dma16(__amdgpu_buffer_rsrc_t rs, uint32_t voff, uint32_t soff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
-                 :
-                 : "v"(voff), "s"(rs), "s"(lds), "s"(soff)
-                 : "memory");
+    if constexpr (NT)
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen nt lds"
+                     :
+                     : "v"(voff), "s"(rs), "s"(lds), "s"(soff)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
+                     :
+                     : "v"(voff), "s"(rs), "s"(lds), "s"(soff)
+                     : "memory");
 }
 __device__ __forceinline__ void lds_dma4(__amdgpu_buffer_rsrc_t rs, uint32_t voff, uint32_t soff, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %3 offen lds"
@@ -535,7 +543,7 @@ __device__ __forceinline__ TileAt find_tile(const TileTable &tt, int v, int tile
 // that pad an expert's last tile, the clock under load, and silu with the
 // quantization between tiles (without it 899 us up), which one wave on a SIMD
 // cannot hide.  24576 rows on 64 experts of d = 2048, h = 1408: 176 + 90 us.
-template <int NB, bool MAP>
+template <int NB, bool MAP, bool NT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx8_tile_kernel(Mx8Args p) {
     constexpr int BM = 256, BN = 256 / NB, WGN = 2, NW = 4, S = 2;
     constexpr int WTM = 128, WTN = BN / WGN, TM = WTM / 32, TN = WTN / 32;
@@ -662,7 +670,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             lds_dma16(c.a, (MAP ? c.aoff[MAP ? part : 0] : q.row + part * step32) | q.out, q.k, dst + part * 4096);
         } else {
             const int b = (part - 8) / (8 / NB), i = (part - 8) % (8 / NB);
-            lds_dma16(b ? c.b1 : c.b0, (q.row + i * step32) | q.out, q.k, dst + kABytes + b * kBBytes + i * 4096);
+            lds_dma16<NT>(b ? c.b1 : c.b0, (q.row + i * step32) | q.out, q.k, dst + kABytes + b * kBBytes + i * 4096);
         }
     };
     auto issue_scales = [&](const Source &c, const Plan &q, int slot) {
@@ -919,11 +927,16 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 
 template <int NB, bool MAP>
 hipError_t launch_tile(const Mx8Args &p, hipStream_t s) {
+    // Weights that one row tile reads go past the caches: 64 experts of d = 2048, h =
+    // 1408 with 40 rows 82 + 47 -> 78 + 43 us, of d = 4096, h = 1024 with 62 rows 123 +
+    // 72 -> 117 + 71; with two row tiles they meet again (384 rows 162 + 88 -> 173 + 98).
+    const bool once = p.g.extent <= 128 * std::min<int64_t>(p.g.G, p.g.extent);
     constexpr int BM = 256, BN = 256 / NB;
     const int64_t tiles = p.g.extent / BM + std::min<int64_t>(p.g.G, p.g.extent);
     const int64_t grid = std::min<int64_t>(2 * tiles * ((p.g.N + BN - 1) / BN), kComputeUnits);
     if (grid <= 0) return hipSuccess;
-    hipLaunchKernelGGL((mx8_tile_kernel<NB, MAP>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+    if (once) hipLaunchKernelGGL((mx8_tile_kernel<NB, MAP, true>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((mx8_tile_kernel<NB, MAP, false>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
