@@ -595,7 +595,8 @@ _F8, _U8 = torch.float8_e4m3fn, torch.uint8
 
 
 _HERE_ALREADY = contextlib.nullcontext()
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _on_device(*ts: Optional[torch.Tensor]):
@@ -614,19 +615,29 @@ def _on_device(*ts: Optional[torch.Tensor]):
 
 def _stream_on(stream, like: torch.Tensor) -> int:
     """The caller's stream, or the current one of the tensors' device."""
-    if stream is None and _raw_stream is not None and like.is_cuda:
+    if stream is None and like.is_cuda:
         return _raw_stream(like.get_device())
     return _stream(stream)
 
 
+def _allocating_on(stream, like: torch.Tensor):
+    """Context in which torch allocates for a call on `stream` (None: the current
+    one).  torch hands memory that was freed on a stream out again at once, to
+    that stream: taken on the current stream, a block may still be written by
+    what is queued there while a call on another stream uses it."""
+    if stream is None or not like.is_cuda or _stream(stream) == _raw_stream(like.get_device()):
+        return _HERE_ALREADY
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    return torch.cuda.stream(stream)
+
+
 def _workspace(ws: Optional[torch.Tensor], need: int, like: torch.Tensor, stream=None):
-    """(tensor, bytes): the caller's workspace, or one of `need` bytes that torch
-    does not hand out again before the call's stream is done with it."""
+    """(tensor, bytes): the caller's workspace, or one of `need` bytes that belongs
+    to the call's stream."""
     if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
-        if stream is not None and like.is_cuda:
-            ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                             else torch.cuda.ExternalStream(_stream(stream), device=like.device))
+        with _allocating_on(stream, like):
+            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
     return ws, ws.numel() * ws.element_size()
 
 

@@ -1,0 +1,87 @@
+"""Calls on streams that are not the current one: whose memory their workspaces
+are, and the results of two callers at once."""
+import pytest
+import torch
+
+import _block_ref as br
+from _helpers import need_gpu
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module")
+def xm():
+    need_gpu()
+    import padding_free_expert_amd as m
+    assert m.xmoe_query_device(0)
+    return m
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+@pytest.fixture
+def taken(xm, monkeypatch):
+    """(address, bytes) of every workspace that a call allocates."""
+    seen, inner = [], xm._workspace
+
+    def spy(ws, need, like, stream=None):
+        t, n = inner(ws, need, like, stream)
+        if ws is None:
+            seen.append((t.data_ptr(), n))
+        return t, n
+
+    monkeypatch.setattr(xm, "_workspace", spy)
+    return seen
+
+
+def _freed(need):
+    """Address of a block of `need` bytes that was just freed on the current stream,
+    and that the next allocation there is given."""
+    a = torch.empty(need, dtype=torch.uint8, device="cuda")
+    at = a.data_ptr()
+    del a
+    b = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert b.data_ptr() == at
+    return at
+
+
+@pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
+def test_workspaces_on_another_stream(xm, taken, handle):
+    """A call on another stream does not take the block that the current stream gave
+    back, and has the bits of the call on the current one."""
+    T, d, E, k = 4096, 2048, 64, 6
+    g = _gen(1)
+    s, dy = (torch.randn((T, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    gamma = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    rstd = torch.rsqrt(s.float().square().mean(1) + EPS)
+    logits = torch.randn((T, E), generator=g, device="cuda")
+    ids = torch.topk(logits, k, 1).indices.to(torch.int32)
+    st = torch.cuda.Stream()
+    out = []
+    for stream in (None, st.cuda_stream if handle else st):
+        dx, dg = torch.empty_like(s), torch.empty(d, device="cuda")
+        loss, counts = torch.empty(1, device="cuda"), torch.empty((1, E), dtype=torch.int32, device="cuda")
+        coef = torch.empty((1, E), device="cuda")
+        calls = (
+            (xm.xmoe_add_rmsnorm_bwd_workspace_size(T, d, s.dtype),
+             lambda: xm.xmoe_add_rmsnorm_bwd(dy, None, s, gamma, rstd, dx, dg, stream=stream)),
+            (xm.xmoe_balance_loss_workspace_size(T, E),
+             lambda: xm.xmoe_balance_loss(logits, ids, 0.1, loss, counts, coef, stream=stream)))
+        torch.cuda.synchronize()
+        for need, call in calls:
+            at = _freed(need)
+            del taken[:]
+            call()
+            (ws, n), = taken
+            assert n >= need
+            if stream is not None:
+                assert ws + n <= at or at + need <= ws, "took the current stream's block"
+        torch.cuda.synchronize()
+        out.append((dx, dg, loss, counts, coef))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
