@@ -267,9 +267,9 @@ def xmoe_route(x, wg, k: int, topk_ids, topk_w, logits, inv_temperature: float =
     _shape(logit_bias, (E,), "logit_bias", _F32)
     _shape(select_bias, (E,), "select_bias", _F32)
     need = xmoe_route_workspace_size(T, d, E, x.dtype)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    nbytes = 0
+    if workspace is not None or need > 0:
+        workspace, nbytes = _workspace(workspace, need, x, stream)
     _check(_lib_route(_ptr(x), _ptr(wg), _dt(x), T, d, E, k, inv_temperature, _ptr(logit_bias),
                       _ptr(select_bias), _ptr(topk_ids), _ptr(topk_w), _ptr(logits), _ptr(workspace), nbytes,
                       _stream(stream)),

@@ -64,3 +64,16 @@ def test_a_callers_workspace_is_used_as_it_is(xm, allocations):
     mine = torch.zeros(64, dtype=torch.uint8)
     ws, n = xm._workspace(mine, 1000, Like(), Stream(9))
     assert ws is mine and n == 64 and allocations == []
+
+
+def test_the_gates_workspace_belongs_to_the_calls_stream(xm, allocations, monkeypatch):
+    T, d, E, k = 6, 64, 8, 2
+    x = torch.zeros((T, d), dtype=torch.bfloat16)
+    wg, ids = torch.zeros((d, E), dtype=torch.bfloat16), torch.zeros((T, k), dtype=torch.int32)
+    w, logits = torch.zeros((T, k)), torch.zeros((T, E))
+    inner = xm._workspace
+    monkeypatch.setattr(xm, "_workspace", lambda ws, need, like, stream=None: inner(ws, need, Like(), stream))
+    monkeypatch.setattr(xm, "xmoe_route_workspace_size", lambda *a: 1000)
+    with pytest.raises(ValueError, match="device tensors"):   # what follows the workspace: the pointers
+        xm.xmoe_route(x, wg, k, ids, w, logits, stream=Stream(9))
+    assert allocations == [9]
