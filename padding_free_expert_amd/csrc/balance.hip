@@ -14,7 +14,11 @@
 // sequences both only go forward, so no two pieces share a row and the rows
 // number at most chunks + S.  A second kernel adds a sequence's rows in order and
 // writes counts and coef; its last block to end adds the blocks' losses in
-// order.  Nothing depends on the order in which blocks run.  The logits are read
+// order.  Nothing depends on the order in which blocks run.  S' comes from the
+// counted tokens of every sequence, whose pieces are added side by side, since a
+// sequence may be masked over any number of them: 2^20 tokens of 16 experts in two
+// sequences 52 us, one of them masked or not (379 and 50 where a thread looked for
+// a sequence's first counted piece).  The logits are read
 // once here, once in the backward, which writes the gradient.  Bound by latency:
 // 4096 tokens of 64 experts take 3.7 + 6.2 us and 3.4 us back, most of it launch,
 // first loads and the hand-over between compute units; 32768 of 160 experts in
@@ -47,12 +51,22 @@ constexpr int kFinalExperts = 32;
 inline int final_blocks(int E) { return (E + kFinalExperts - 1) / kFinalExperts; }
 inline size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
+// S' needs the counted tokens of all sequences in every block of the second
+// kernel.  It adds them up itself, 16 lanes a sequence, where that is few loads;
+// else a kernel between the two does, once.
+constexpr int kFewSequences = 64;
+constexpr int64_t kFewChunks = 512;
+inline bool counts_itself(int64_t T, int S) {
+    return S == 1 || (S <= kFewSequences && T <= kFewChunks * chunk_tokens(T));
+}
+
 struct BalanceWs {
     float *psum;      // [rows, E]
     int32_t *csum;    // [rows, E]
     int32_t *nsum;    // [rows]
     double *part_loss; // [S, blocks of experts]
     int32_t *ticket;  // [1]
+    int32_t *nseq;    // [S]; nullptr: the second kernel counts by itself
     size_t bytes;
 };
 BalanceWs balance_ws(void *ws, int64_t T, int E, int S) {
@@ -70,6 +84,7 @@ BalanceWs balance_ws(void *ws, int64_t T, int E, int S) {
     b.nsum = reinterpret_cast<int32_t *>(take(rows * 4));
     b.part_loss = reinterpret_cast<double *>(take(static_cast<size_t>(S) * final_blocks(E) * 8));
     b.ticket = reinterpret_cast<int32_t *>(take(4));
+    b.nseq = counts_itself(T, S) ? nullptr : reinterpret_cast<int32_t *>(take(static_cast<size_t>(S) * 4));
     b.bytes = at;
     return b;
 }
@@ -237,6 +252,22 @@ __device__ __forceinline__ void piece_rows(const int32_t *off, int s, int64_t T,
     *hi = a < b ? (b - 1) / chunk + s + 1 : 0;
 }
 
+// Counted tokens of each sequence, a block each, where the second kernel does not
+// add them up by itself.
+__global__ __launch_bounds__(256) void balance_count_kernel(int64_t T, const int32_t *off, int chunk, BalanceWs ws) {
+    __shared__ int32_t wn[4];
+    int64_t lo, hi;
+    piece_rows(off, blockIdx.x, T, chunk, &lo, &hi);
+    int32_t n = 0;
+#pragma unroll 4
+    for (int64_t b = lo + threadIdx.x; b < hi; b += 256) n += ws.nsum[b];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, 64);
+    if (threadIdx.x % 64 == 0) wn[threadIdx.x / 64] = n;
+    __syncthreads();
+    if (threadIdx.x == 0) ws.nseq[blockIdx.x] = wn[0] + wn[1] + wn[2] + wn[3];
+}
+
 // A block per sequence and 32 experts.  The rows' values are asked for first;
 // what the counts need (n_s, S') comes beside them.
 __global__ __launch_bounds__(1024) void balance_final_kernel(int64_t T, int E, int k, const int32_t *off, int S,
@@ -262,16 +293,28 @@ __global__ __launch_bounds__(1024) void balance_final_kernel(int64_t T, int E, i
             c += ws.csum[b * E + e];
         }
     }
-    for (int64_t b = lo + threadIdx.x; b < hi; b += 1024) n += ws.nsum[b];
-    // S': sequences that count a token.  A sequence's first piece mostly tells.
-    int some = 0;
-    if (S > 1) {
+    int some = 0;  // S': sequences that count a token
+    if (S == 1) {
+        for (int64_t b = lo + threadIdx.x; b < hi; b += 1024) n += ws.nsum[b];
+    } else if (ws.nseq) {
         for (int i = threadIdx.x; i < S; i += 1024) {
-            int64_t a, z;
-            piece_rows(off, i, T, chunk, &a, &z);
-            int any = 0;
-            for (; a < z && !any; ++a) any = ws.nsum[a] > 0;
-            some += any;
+            const int32_t v = ws.nseq[i];
+            some += v > 0;
+            n = i == s ? v : n;
+        }
+    } else {
+        constexpr int L = 1024 / kFewSequences;  // lanes of a sequence
+        const int i = threadIdx.x / L;
+        int64_t a = 0, z = 0;
+        if (i < S) piece_rows(off, i, T, chunk, &a, &z);
+        int32_t v = 0;
+#pragma unroll 4
+        for (a += threadIdx.x % L; a < z; a += L) v += ws.nsum[a];
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+        if (threadIdx.x % L == 0) {
+            some = v > 0;
+            n = i == s ? v : 0;
         }
     }
     sp[threadIdx.x % W][part] = p;
@@ -422,8 +465,12 @@ hipError_t launch_balance_loss(const float *logits, const int32_t *ids, int64_t 
     else if (many && E <= 128) XMOE_BALANCE_PART(8, 16);
     else XMOE_BALANCE_SHAPE(E, XMOE_BALANCE_PART);
 #undef XMOE_BALANCE_PART
-    const hipError_t e = hipGetLastError();
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (w.nseq) {
+        hipLaunchKernelGGL(balance_count_kernel, dim3(static_cast<unsigned>(S)), dim3(256), 0, st, T, seq_offsets, chunk, w);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     hipLaunchKernelGGL(balance_final_kernel, dim3(static_cast<unsigned>(S * final_blocks(E))), dim3(1024), 0, st, T, E, k, seq_offsets,
                        S, chunk, alpha, w, loss, counts, coef);
     return hipGetLastError();
