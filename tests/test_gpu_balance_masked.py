@@ -12,7 +12,8 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("T,S,E,k", [
     (40000, 2, 16, 2), (40000, 16, 33, 3), (40000, 17, 16, 2), (40000, 63, 8, 2), (40000, 64, 64, 6), (40000, 65, 16, 2),
-    (40000, 300, 8, 1), (65536, 3, 8, 2), (65537, 3, 8, 2), (200000, 5, 16, 2)])
+    (40000, 300, 8, 1), (65536, 3, 8, 2), (65537, 3, 8, 2), (200000, 5, 16, 2),
+    (5000, 200, 1024, 8), (9000, 4096, 64, 2)])
 def test_masked_sequences(xm, T, S, E, k):  # noqa: F811
     """Every second sequence masked, the first one too; then all but the last
     token; sequences up to the whole batch."""
