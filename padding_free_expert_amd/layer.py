@@ -22,6 +22,38 @@ from . import (PFT, mx8_scale_shape, xmoe_add_rmsnorm, xmoe_add_rmsnorm_bwd, xmo
                xmoe_route_bwd_workspace_size, xmoe_route_workspace_size)
 
 
+def _on(stream, device) -> torch.cuda.Stream:
+    """The caller's stream (or its handle), or the current one of the device."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+
+
+class _Written:
+    """Orders what reads a layer's own copies of the weights, on any stream, behind
+    what wrote them.  A capture neither records nor waits here (an event of one
+    side of a capture cannot be waited for on the other): what a graph reads or
+    writes is in the order in which it is captured and replayed."""
+
+    def __init__(self):
+        self.event, self.behind = None, set()
+
+    @staticmethod
+    def _capturing(stream) -> bool:
+        with torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
+
+    def wrote(self, stream) -> None:
+        if not self._capturing(stream):
+            self.event, self.behind = torch.cuda.Event(), {stream.cuda_stream}
+            self.event.record(stream)
+
+    def read(self, stream) -> None:
+        if self.event is not None and stream.cuda_stream not in self.behind and not self._capturing(stream):
+            stream.wait_event(self.event)
+            self.behind.add(stream.cuda_stream)
+
+
 class PaddingFreeMoE:
     """Buffers and call sequence for one layer of T tokens.
 
@@ -450,22 +482,29 @@ class MoEBlock8:
             self.sh_act, self.sh_acts = rows(T, hs)
             self.sh_y = torch.empty((T, d), **bf)
             self.side = torch.cuda.Stream(device=dev)
+        self.written = _Written()
         self.refresh_weights()
 
     def refresh_weights(self, stream=None) -> None:
-        """Quantize the weights (the tensors in the weights dict) again."""
+        """Quantize the weights (the tensors in the weights dict) again.  Later
+        forwards wait for it, on whatever stream they are; the caller orders it
+        behind the update of the weights and behind forwards that still read the
+        old ones, if those are on other streams."""
         w = self.w
+        stream = _on(stream, self.device)
         pairs = [(w["w1"], self.w1q), (w["w3"], self.w3q), (w["w2"], self.w2q)]
         if self.shared:
             pairs += [(w[n].unsqueeze(0), q) for n, q in (("s1", self.s1q), ("s3", self.s3q), ("s2", self.s2q))]
         for t, (q, s) in pairs:
             xmoe_mx8_quantize_weights(t, q, s, stream=stream)
+        self.written.wrote(stream)
 
     def forward(self, x: torch.Tensor, residual=None, stream=None):
         """(out, sum)."""
         w = self.w
-        main = stream if stream is not None else torch.cuda.current_stream(self.device)
+        main = _on(stream, self.device)
         side = self.side if self.shared and self.overlap else main
+        self.written.read(main)
         xmoe_add_rmsnorm(x, residual, w["norm"], self.eps, self.sum, self.y, self.yq, self.yqs, stream=main)
         if self.shared:
             if side is not main:

@@ -77,3 +77,112 @@ def test_the_gates_workspace_belongs_to_the_calls_stream(xm, allocations, monkey
     with pytest.raises(ValueError, match="device tensors"):   # what follows the workspace: the pointers
         xm.xmoe_route(x, wg, k, ids, w, logits, stream=Stream(9))
     assert allocations == [9]
+
+
+class Device:
+    """Stand-ins for what a layer launches and for the streams it launches on: every
+    write and read of its weights must be ordered, by the stream or by an event."""
+
+    def __init__(self, monkeypatch, names):
+        from padding_free_expert_amd import layer
+        self.log, self.current, dev = [], self.stream(1), self
+        self.capturing = set()
+
+        class Event:
+            def record(self, stream):
+                dev.log.append(("record", self, stream.cuda_stream))
+
+        @contextlib.contextmanager
+        def enter(s):
+            was, dev.current = dev.current, s
+            yield
+            dev.current = was
+
+        for n in names:
+            monkeypatch.setattr(layer, n, lambda *a, stream=None, name=n, **kw: dev.log.append(
+                (name, a, (stream or dev.current).cuda_stream)))
+        monkeypatch.setattr(torch.cuda, "Event", Event)
+        monkeypatch.setattr(torch.cuda, "Stream", lambda device=None: dev.stream(77))
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: dev.stream(h))
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: dev.current)
+        monkeypatch.setattr(torch.cuda, "stream", enter)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: dev.current.cuda_stream in dev.capturing)
+
+    def stream(self, handle):
+        dev = self
+
+        class S(Stream):
+            def wait_event(self, e):
+                dev.log.append(("wait", e, self.cuda_stream))
+
+            def wait_stream(self, other):
+                dev.log.append(("join", other.cuda_stream, self.cuda_stream))
+        return S(handle)
+
+    def ordered(self, writes, read):
+        """The last call of `writes` is followed by its stream's event, and that is
+        waited for before every later call of `read` on another stream."""
+        event = home = None
+        seen = set()
+        for name, what, at in self.log:
+            if name == writes:
+                event, home, seen = None, at, {at}
+            elif name == "record" and at == home:
+                event = what
+            elif name == "wait" and what is event:
+                seen.add(at)
+            elif name == "join" and what in seen:
+                seen.add(at)
+            elif name == read and at not in seen:
+                return False
+        return home is not None
+
+
+BLOCK8 = ["xmoe_mx8_quantize_weights", "xmoe_add_rmsnorm", "xmoe_route", "xmoe_build_pft", "xmoe_expert_ffn_up_mx8",
+          "xmoe_expert_ffn_down_mx8", "xmoe_combine"]
+
+
+def _weights(dt=torch.bfloat16, shared=True, T=4, d=64, E=4, h=32):
+    z = torch.zeros
+    w = dict(wg=z((d, E), dtype=dt), w1=z((E, d, h), dtype=dt), w3=z((E, d, h), dtype=dt), w2=z((E, h, d), dtype=dt),
+             norm=z(d, dtype=dt))
+    if shared:
+        w.update(s1=z((d, h), dtype=dt), s3=z((d, h), dtype=dt), s2=z((h, d), dtype=dt))
+    return w, z((T, d), dtype=dt)
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_8_bit_weights_are_read_behind_their_quantization(xm, monkeypatch, shared):
+    """Whatever stream quantizes them and whatever stream the forward is on."""
+    from padding_free_expert_amd.layer import MoEBlock8
+    dev = Device(monkeypatch, BLOCK8)
+    w, x = _weights(shared=shared)
+    order = lambda: dev.ordered("xmoe_mx8_quantize_weights", "xmoe_expert_ffn_up_mx8")
+    block = MoEBlock8(w, 4, 2)                 # on stream 1
+    block.forward(x)
+    assert order() and not any(n == "wait" for n, _, _ in dev.log)
+    block.forward(x, stream=dev.stream(2))
+    assert order()
+    n = len(dev.log)
+    block.forward(x, stream=dev.stream(2))     # one wait a stream is enough
+    assert order() and not any(e[0] == "wait" for e in dev.log[n:])
+    block.refresh_weights(stream=dev.stream(3))
+    for s in (None, dev.stream(2), dev.stream(3)):
+        block.forward(x, stream=s)
+        assert order()
+
+
+def test_a_captured_quantization_or_forward_waits_for_no_event_outside(xm, monkeypatch):
+    """An event of one side of a capture cannot be waited for on the other."""
+    from padding_free_expert_amd.layer import MoEBlock8
+    dev = Device(monkeypatch, BLOCK8)
+    w, x = _weights()
+    block = MoEBlock8(w, 4, 2)
+    dev.capturing.add(2)
+    n = len(dev.log)
+    block.forward(x, stream=dev.stream(2))
+    block.refresh_weights(stream=dev.stream(2))
+    assert not any(e[0] in ("wait", "record") for e in dev.log[n:])
+    dev.capturing.clear()
+    block.forward(x, stream=dev.stream(2))
+    assert any(e[0] == "wait" for e in dev.log[n:])

@@ -85,3 +85,44 @@ def test_workspaces_on_another_stream(xm, taken, handle):
         out.append((dx, dg, loss, counts, coef))
     for a, b in zip(*out):
         assert torch.equal(a, b)
+
+
+def _serving(seed=0):
+    import workloads
+    wl = workloads.Workload("streams8", "bf16", T=40, d=512, E=64, h=1408, k=6, n_shared=1, h_shared=512, backward=True)
+    inp = {k: v.cuda() for k, v in workloads.generate(wl).items() if v is not None}
+    w = {k: inp[k] for k in ("wg", "w1", "w3", "w2", "s1", "s3", "s2")}
+    w["norm"] = torch.ones(wl.d, dtype=torch.bfloat16, device="cuda")
+    return wl, w, inp["x"]
+
+
+def _busy(ms=10):
+    """Work of some milliseconds queued on the current stream."""
+    a = torch.ones((8192, 8192), dtype=torch.bfloat16, device="cuda")
+    for _ in range(ms):
+        a @ a
+
+
+def test_a_forward_on_another_stream_behind_the_quantization(xm):
+    """Constructed, or refreshed, behind queued work on one stream, and run at once on
+    another: the bits of a block that is waited for."""
+    from padding_free_expert_amd.layer import MoEBlock8
+    wl, w, x = _serving()
+    want = MoEBlock8(w, wl.T, wl.k).forward(x)[0].clone()
+    st, rt = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _busy()
+    block = MoEBlock8(w, wl.T, wl.k)
+    out, _ = block.forward(x, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    for n in ("w1", "w3", "w2", "s1", "s3", "s2"):
+        w[n].mul_(0.5)
+    want = MoEBlock8(w, wl.T, wl.k).forward(x)[0].clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(rt):
+        _busy()
+        block.refresh_weights()
+    out, _ = block.forward(x, stream=st.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
