@@ -119,6 +119,7 @@ class PaddingFreeMoE:
         # stream after dW2.  Whole steps: DeepSeek-MoE-16B shape -1.0%,
         # Zipf-skewed -4%, long batch (1638 rows per expert) +0.4%.
         self.dw13_main = R <= 1024 * Ec
+        self.written = _Written()
         if self.merged:
             self.W1 = torch.empty((Ec, d, h), dtype=dt, device=dev)
             self.W3 = torch.empty((Ec, d, h), dtype=dt, device=dev)
@@ -180,12 +181,14 @@ class PaddingFreeMoE:
         buffers, in place on `stream`.  The merged buffers are copies, so a
         caller that updates the weights (an optimizer step) calls this before
         the next forward; without merging the layer reads the caller's tensors
-        directly and this does nothing.  It allocates nothing, so it can sit
-        inside a captured graph."""
+        directly and this does nothing.  Later passes wait for it, on whatever
+        stream they are; the caller orders it behind passes that still read the
+        old weights, if those are on other streams.  It allocates nothing, so it
+        can sit inside a captured graph."""
         if not self.merged:
             return
         w, E, ns, d, h = self.w, self.E, self.ns, self.d, self.h
-        main = stream if stream is not None else torch.cuda.current_stream(self.device)
+        main = _on(stream, self.device)
         with torch.cuda.stream(main):
             self.W1[:E].copy_(w["w1"])
             self.W3[:E].copy_(w["w3"])
@@ -193,6 +196,7 @@ class PaddingFreeMoE:
             self.W1[E:].copy_(w["s1"].view(d, ns, h).permute(1, 0, 2))
             self.W3[E:].copy_(w["s3"].view(d, ns, h).permute(1, 0, 2))
             self.W2[E:].copy_(w["s2"].view(ns, h, d))
+        self.written.wrote(main)
 
     # views of the unmerged shared-expert weights as a single expert of width n*h_s
     def _shared_w(self):
@@ -200,8 +204,9 @@ class PaddingFreeMoE:
         return w["s1"].unsqueeze(0), w["s3"].unsqueeze(0), w["s2"].unsqueeze(0)
 
     def _streams(self, stream):
-        main = stream if stream is not None else torch.cuda.current_stream(self.device)
+        main = _on(stream, self.device)
         side = self.side if (self.side_shared and self.overlap) else main
+        self.written.read(main)
         return main, side
 
     def forward(self, x: torch.Tensor, stream=None, hook=None, probe=None, seq_offsets=None,

@@ -186,3 +186,29 @@ def test_a_captured_quantization_or_forward_waits_for_no_event_outside(xm, monke
     dev.capturing.clear()
     block.forward(x, stream=dev.stream(2))
     assert any(e[0] == "wait" for e in dev.log[n:])
+
+
+LAYER = ["xmoe_add_rmsnorm", "xmoe_route", "xmoe_build_pft", "xmoe_build_pft_shared", "xmoe_expert_ffn_up",
+         "xmoe_expert_ffn_up_gather", "xmoe_expert_ffn_down", "xmoe_combine", "xmoe_balance_loss", "xmoe_combine_bwd",
+         "xmoe_expert_ffn_bwd", "xmoe_route_bwd", "xmoe_route_bwd_balance", "xmoe_expert_ffn_bwd_dact_gather",
+         "xmoe_expert_ffn_bwd_dw2", "xmoe_expert_ffn_bwd_dw13_gather", "xmoe_expert_ffn_bwd_dx", "xmoe_dispatch_bwd",
+         "xmoe_add_rmsnorm_bwd"]
+
+
+def test_merged_weights_are_read_behind_their_copies(xm, monkeypatch):
+    from padding_free_expert_amd.layer import PaddingFreeMoE
+    dev = Device(monkeypatch, LAYER)
+    w, x = _weights()
+    m = PaddingFreeMoE(w, 4, 2, merge_shared=True)     # on stream 1
+    for s in (None, dev.stream(2)):
+        n = len(dev.log)
+        m.forward(x, stream=s)
+        m.backward(x, stream=s)
+        waits = [i for i, e in enumerate(dev.log[n:]) if e[0] == "wait"]
+        assert waits == ([] if s is None else [0])
+    m.refresh_weights(stream=dev.stream(3))
+    what, event, at = dev.log[-1]
+    assert (what, at) == ("record", 3)
+    n = len(dev.log)
+    m.backward(x, stream=dev.stream(2))
+    assert dev.log[n] == ("wait", event, 2)
