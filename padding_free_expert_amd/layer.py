@@ -29,6 +29,19 @@ def _on(stream, device) -> torch.cuda.Stream:
     return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
 
 
+def _need(t, shape, dtypes, name: str, device) -> None:
+    """What the calls of a pass would refuse, asked before its first launch: an
+    exception between two launches leaves streams that nothing joins again."""
+    if t is None:
+        return
+    if t.shape != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, the layer needs {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, the layer needs {dtypes[0]}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor on {device} is needed")
+
+
 class _Written:
     """Orders what reads a layer's own copies of the weights, on any stream, behind
     what wrote them.  A capture neither records nor waits here (an event of one
@@ -222,6 +235,12 @@ class PaddingFreeMoE:
         w = self.w
         mark = hook or (lambda name: None)
         around = probe or (lambda name, s: None)
+        _need(x, (self.T, self.d), (self.dtype,), "x", self.device)
+        if self.balance_alpha > 0:
+            if self.n_seq > 1 and seq_offsets is None:
+                raise ValueError("seq_offsets is required for more than one sequence")
+            _need(seq_offsets, (self.n_seq + 1,), (torch.int32,), "seq_offsets", self.device)
+            _need(token_mask, (self.T,), (torch.bool, torch.uint8), "token_mask", self.device)
         main, side = self._streams(stream)
         keep = self.backward_enabled and not self.lean
         if self.side_shared:
@@ -238,8 +257,6 @@ class PaddingFreeMoE:
         mark("route")
         bs = main
         if self.balance_alpha > 0:
-            if self.n_seq > 1 and seq_offsets is None:
-                raise ValueError("seq_offsets is required for more than one sequence")
             self.seq_offsets, self.token_mask = seq_offsets, token_mask
             if self.overlap and self.gside is not None:
                 bs = self.gside
@@ -275,6 +292,9 @@ class PaddingFreeMoE:
         (None: 1)."""
         w = self.w
         mark = hook or (lambda name: None)
+        _need(dy, (self.T, self.d), (self.dtype,), "dy", self.device)
+        if self.balance_alpha > 0:
+            _need(dloss, (1,), (torch.float32,), "dloss", self.device)
         main, side = self._streams(stream)
         gs = self.gside if self.overlap else main
         dx_add = None

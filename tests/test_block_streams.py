@@ -212,3 +212,49 @@ def test_merged_weights_are_read_behind_their_copies(xm, monkeypatch):
     n = len(dev.log)
     m.backward(x, stream=dev.stream(2))
     assert dev.log[n] == ("wait", event, 2)
+
+
+@pytest.mark.parametrize("kw,err", [
+    (dict(), "seq_offsets"), (dict(seq_offsets=torch.zeros(2, dtype=torch.int32)), "seq_offsets"),
+    (dict(seq_offsets=torch.zeros(3)), "seq_offsets"), (dict(seq_offsets=torch.zeros(6, dtype=torch.int32)[::2]), "seq_offsets"),
+    (dict(token_mask=torch.zeros(5, dtype=torch.bool)), "token_mask"), (dict(token_mask=torch.zeros(4)), "token_mask"),
+    (dict(token_mask=torch.zeros(4, dtype=torch.bool, device="meta")), "token_mask"),
+    (dict(x=torch.zeros((3, 64), dtype=torch.bfloat16)), "x"), (dict(x=torch.zeros((4, 64))), "x")])
+def test_a_refused_forward_launches_nothing(xm, monkeypatch, kw, err):
+    from padding_free_expert_amd.layer import PaddingFreeMoE
+    dev = Device(monkeypatch, LAYER)
+    w, x = _weights()
+    m = PaddingFreeMoE(w, 4, 2, balance_alpha=0.1, n_seq=2)
+    good = dict(x=x, seq_offsets=torch.zeros(3, dtype=torch.int32))
+    bad = {**({"x": x} if not kw else good), **kw}
+    del dev.log[:]
+    with pytest.raises((ValueError, TypeError), match=err):
+        m.forward(**bad)
+    assert dev.log == []
+    m.forward(**good)
+    assert dev.log
+
+
+@pytest.mark.parametrize("kw,err", [(dict(dloss=torch.zeros(())), "dloss"), (dict(dloss=torch.zeros(1, dtype=torch.bfloat16)), "dloss"),
+                                    (dict(dy=torch.zeros((4, 32), dtype=torch.bfloat16)), "dy")])
+def test_a_refused_backward_launches_nothing(xm, monkeypatch, kw, err):
+    from padding_free_expert_amd.layer import PaddingFreeMoE
+    dev = Device(monkeypatch, LAYER)
+    w, x = _weights()
+    m = PaddingFreeMoE(w, 4, 2, balance_alpha=0.1)
+    m.forward(x)
+    del dev.log[:]
+    with pytest.raises((ValueError, TypeError), match=err):
+        m.backward(**{**dict(dy=x), **kw})
+    assert dev.log == []
+    m.backward(x, dloss=torch.zeros(1))
+    assert dev.log
+
+
+def test_the_layer_without_the_loss_ignores_its_arguments(xm, monkeypatch):
+    from padding_free_expert_amd.layer import PaddingFreeMoE
+    Device(monkeypatch, LAYER)
+    w, x = _weights()
+    m = PaddingFreeMoE(w, 4, 2)
+    m.forward(x, token_mask=torch.zeros(9))
+    m.backward(x, dloss=torch.zeros(9))
