@@ -467,9 +467,9 @@ class MoEBlock:
 class MoEBlock8:
     """The same block for serving, its experts in 8 bits: the norm leaves y for the
     gate and y in 8 bits for the experts, whose weights are quantized once at
-    construction (again by refresh_weights() after they change).  bf16 weights
-    as PaddingFreeMoE takes them, with "norm"; d, h and the shared width
-    multiples of 32.  Shared experts run on a second stream beside the routed
+    construction (again by refresh_weights() after they change).  Weights as
+    PaddingFreeMoE takes them, with "norm": the gate's and the norm's in bf16,
+    the experts' in bf16 or fp32; d, h and the shared width multiples of 32.  Shared experts run on a second stream beside the routed
     ones.  Holds the buffers of T tokens."""
 
     def __init__(self, weights: Dict[str, torch.Tensor], T: int, k: int, inv_tau: float = 1.0, eps: float = 1e-6,
@@ -477,6 +477,9 @@ class MoEBlock8:
         self.w, self.T, self.k, self.inv_tau, self.eps, self.overlap = weights, T, k, inv_tau, eps, overlap
         wg, w1 = weights["wg"], weights["w1"]
         dev, dt = wg.device, wg.dtype
+        for n in ("wg", "norm"):
+            if weights[n].dtype != torch.bfloat16:
+                raise TypeError(f"{n}: dtype {weights[n].dtype}, the block needs {torch.bfloat16}")
         self.device, (self.d, self.E), self.h = dev, wg.shape, w1.shape[2]
         d, E, h, R = self.d, self.E, self.h, T * k
         self.shared = weights.get("s1") is not None

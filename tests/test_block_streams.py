@@ -258,3 +258,16 @@ def test_the_layer_without_the_loss_ignores_its_arguments(xm, monkeypatch):
     m = PaddingFreeMoE(w, 4, 2)
     m.forward(x, token_mask=torch.zeros(9))
     m.backward(x, dloss=torch.zeros(9))
+
+
+def test_the_serving_block_refuses_what_its_forward_could_not_take(xm, monkeypatch):
+    """Its rows are bf16, so the gate and the norm are; the experts' weights are
+    quantized from either type."""
+    from padding_free_expert_amd.layer import MoEBlock8
+    dev = Device(monkeypatch, BLOCK8)
+    w, x = _weights()
+    for bad in (_weights(torch.float32)[0], {**w, "wg": w["wg"].float()}, {**w, "norm": w["norm"].float()}):
+        with pytest.raises(TypeError, match="wg|norm"):
+            MoEBlock8(bad, 4, 2)
+    assert dev.log == []
+    MoEBlock8({**w, "w1": w["w1"].float(), "w3": w["w3"].float(), "w2": w["w2"].float()}, 4, 2).forward(x)
