@@ -126,3 +126,46 @@ def test_a_forward_on_another_stream_behind_the_quantization(xm):
     out, _ = block.forward(x, stream=st.cuda_stream)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_two_callers_at_once(xm):
+    """Calls that allocate their workspaces, on two streams with no order between
+    them, each on inputs and outputs of its own: the bits each has alone."""
+    T, d, E, k, S = 4096, 2048, 64, 6, 3
+    off = torch.tensor([0, 1000, 1001, T - 5], dtype=torch.int32, device="cuda")
+    gamma = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+
+    class Caller:
+        def __init__(self, seed):
+            g = _gen(seed)
+            self.s, self.dy = (torch.randn((T, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+            self.rstd = torch.rsqrt(self.s.float().square().mean(1) + EPS)
+            self.logits = torch.randn((T, E), generator=g, device="cuda")
+            self.ids = torch.topk(self.logits, k, 1).indices.to(torch.int32)
+            self.out = self.buffers()
+
+        @staticmethod
+        def buffers():
+            return dict(dx=torch.empty((T, d), dtype=torch.bfloat16, device="cuda"), dg=torch.empty(d, device="cuda"),
+                        loss=torch.empty(1, device="cuda"), counts=torch.empty((S, E), dtype=torch.int32, device="cuda"),
+                        coef=torch.empty((S, E), device="cuda"))
+
+        def call(self, o, stream=None):
+            xm.xmoe_add_rmsnorm_bwd(self.dy, None, self.s, gamma, self.rstd, o["dx"], o["dg"], stream=stream)
+            xm.xmoe_balance_loss(self.logits, self.ids, 0.1, o["loss"], o["counts"], o["coef"], off, stream=stream)
+
+    callers, ss = [Caller(1), Caller(2)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    alone = []
+    for c in callers:
+        alone.append(c.buffers())
+        c.call(alone[-1])
+        torch.cuda.synchronize()
+    assert not torch.equal(alone[0]["coef"], alone[1]["coef"])
+    _busy(2)     # what the current stream gives back meanwhile stays its own
+    for _ in range(10):
+        for c, st in zip(callers, ss):
+            c.call(c.out, stream=st)
+    torch.cuda.synchronize()
+    for c, a in zip(callers, alone):
+        for n, t in c.out.items():
+            assert torch.equal(t, a[n]), n
