@@ -24,6 +24,7 @@
 #include "gemm.hpp"
 #include "kernels.hpp"
 #include "mx8.hpp"
+#include "mx8_choice.hpp"
 
 namespace xmoe {
 
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(256) void mx8_quantize_weights_kernel(const T *__re
 // ------------------------------------------------------------------ products
 
 // one block of the tile kernel for each (a multiple of the XCDs' number)
-constexpr int kComputeUnits = 256;
+constexpr int kComputeUnits = kMxComputeUnits;
 
 // two fp32 -> packed bf16, round to nearest even
 __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
@@ -926,15 +927,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 }
 
 template <int NB, bool MAP>
-hipError_t launch_tile(const Mx8Args &p, hipStream_t s) {
+hipError_t launch_tile(const Mx8Args &p, bool once, hipStream_t s) {
     constexpr int BM = 256, BN = 256 / NB;
     const int64_t cols = (p.g.N + BN - 1) / BN, active = std::min<int64_t>(p.g.G, p.g.extent);
-    // Weights that one row tile reads go past the caches: 64 experts of d = 2048, h =
-    // 1408 with 40 rows 82 + 47 -> 78 + 43 us, of d = 4096, h = 1024 with 62 rows 123 +
-    // 72 -> 117 + 71; with two row tiles they meet again (384 rows 162 + 88 -> 173 + 98).
-    // A launch without a tile for each compute unit keeps to the caches (4 experts
-    // with 64 rows 21 + 16 against 25 + 19, their weights in the last-level cache).
-    const bool once = p.g.extent <= 128 * active && active * cols >= kComputeUnits;
     const int64_t grid = std::min<int64_t>(2 * (p.g.extent / BM + active) * cols, kComputeUnits);
     if (grid <= 0) return hipSuccess;
     if (once) hipLaunchKernelGGL((mx8_tile_kernel<NB, MAP, true>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
@@ -968,23 +963,13 @@ Mx8Args rows_args(const int32_t *offsets, int E, int64_t rows, int N, int K) {
 
 template <int NB>
 hipError_t product(const Mx8Args &p, hipStream_t s) {
-    // Up + down, 64 experts of d = 2048, h = 1408: the stream kernel with 16 rows a
-    // block, with 32, and the tile kernel take at 9 rows an expert 60 + 33, 63 + 33
-    // and 73 + 41 us; at 12 63 + 35, 63 + 33 and 74 + 41; at 16 75 + 41, 64 + 34 and
-    // 74 + 41; at 26 the last two 73 + 40 and 76 + 42; at 28 79 + 43 and 76 + 41; at 40
-    // 116 + 63 and 77 + 43.  With more rows each 32 of them read the weights again,
-    // which pays only where the launch is so small that the tile kernel leaves
-    // compute units idle: three stream blocks for each unit at most (4 such experts of
-    // 64, 96 and 128 rows 13 + 10, 17 + 10 and 23 + 14 us, tiles 21 + 16; 16 experts of
-    // d = 512, h = 256 with 128 and 500 rows 8 + 6 and 21 + 15, tiles 12 + 9 and 13 + 10).
-    const int64_t rows = p.g.extent, active = std::min<int64_t>(p.g.G, rows);
-    const int64_t blocks = (rows / 32 + active) * ((p.g.N + 64 / NB - 1) / (64 / NB));
-    if (rows <= 12 * active) return launch_stream<NB, 1>(p, s);
-    if (rows <= 26 * active || blocks <= 3 * kComputeUnits) return launch_stream<NB, 2>(p, s);
+    const Mx8Choice c = mx8_choose(p.g.extent, p.g.G, p.g.N, NB);
+    if (c.stream == 1) return launch_stream<NB, 1>(p, s);
+    if (c.stream == 2) return launch_stream<NB, 2>(p, s);
     if constexpr (NB == 2) {
-        if (p.map) return launch_tile<2, true>(p, s);
+        if (p.map) return launch_tile<2, true>(p, c.once, s);
     }
-    return launch_tile<NB, false>(p, s);
+    return launch_tile<NB, false>(p, c.once, s);
 }
 
 }  // namespace
