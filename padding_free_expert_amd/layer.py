@@ -8,11 +8,12 @@ Python: every step is a libxmoe kernel.
 """
 from __future__ import annotations
 
+import functools
 from typing import Dict
 
 import torch
 
-from . import (PFT, mx8_scale_shape, xmoe_add_rmsnorm, xmoe_add_rmsnorm_bwd, xmoe_add_rmsnorm_bwd_workspace_size,
+from . import (PFT, _on_device, mx8_scale_shape, xmoe_add_rmsnorm, xmoe_add_rmsnorm_bwd, xmoe_add_rmsnorm_bwd_workspace_size,
                xmoe_balance_loss, xmoe_balance_loss_workspace_size, xmoe_build_pft, xmoe_build_pft_shared,
                xmoe_build_pft_workspace_size, xmoe_combine,
                xmoe_combine_bwd, xmoe_dispatch_bwd, xmoe_expert_ffn_bwd,
@@ -20,6 +21,16 @@ from . import (PFT, mx8_scale_shape, xmoe_add_rmsnorm, xmoe_add_rmsnorm_bwd, xmo
                xmoe_expert_ffn_down, xmoe_expert_ffn_down_mx8, xmoe_expert_ffn_up, xmoe_expert_ffn_up_gather,
                xmoe_expert_ffn_up_mx8, xmoe_mx8_quantize_weights, xmoe_route, xmoe_route_bwd, xmoe_route_bwd_balance,
                xmoe_route_bwd_workspace_size, xmoe_route_workspace_size)
+
+
+def _on_its_device(method):
+    """The library launches on the current device: a layer's passes make its own the
+    current one."""
+    @functools.wraps(method)
+    def run(self, *args, **kw):
+        with _on_device(self.w["wg"]):
+            return method(self, *args, **kw)
+    return run
 
 
 def _on(stream, device) -> torch.cuda.Stream:
@@ -188,6 +199,7 @@ class PaddingFreeMoE:
                 self._ds3 = torch.empty((1, d, hs), dtype=dt, device=dev)
                 self._ds2 = torch.empty((1, hs, d), dtype=dt, device=dev)
 
+    @_on_its_device
     def refresh_weights(self, stream=None) -> None:
         """Merged layout only: copy the routed and shared weights (the tensors in
         the weights dict, in their own layouts) into the layer's [E + n, ...]
@@ -222,6 +234,7 @@ class PaddingFreeMoE:
         self.written.read(main)
         return main, side
 
+    @_on_its_device
     def forward(self, x: torch.Tensor, stream=None, hook=None, probe=None, seq_offsets=None,
                 token_mask=None) -> torch.Tensor:
         """seq_offsets int32 [n_seq + 1] and token_mask bool [T]: the tokens that the
@@ -287,6 +300,7 @@ class PaddingFreeMoE:
         self.x = x
         return self.y
 
+    @_on_its_device
     def backward(self, dy: torch.Tensor, stream=None, hook=None, dloss=None) -> torch.Tensor:
         """dloss: upstream gradient of the balance loss, fp32 [1] on the device
         (None: 1)."""
@@ -513,6 +527,7 @@ class MoEBlock8:
         self.written = _Written()
         self.refresh_weights()
 
+    @_on_its_device
     def refresh_weights(self, stream=None) -> None:
         """Quantize the weights (the tensors in the weights dict) again.  Later
         forwards wait for it, on whatever stream they are; the caller orders it
@@ -527,6 +542,7 @@ class MoEBlock8:
             xmoe_mx8_quantize_weights(t, q, s, stream=stream)
         self.written.wrote(stream)
 
+    @_on_its_device
     def forward(self, x: torch.Tensor, residual=None, stream=None):
         """(out, sum)."""
         w = self.w

@@ -271,3 +271,31 @@ def test_the_serving_block_refuses_what_its_forward_could_not_take(xm, monkeypat
             MoEBlock8(bad, 4, 2)
     assert dev.log == []
     MoEBlock8({**w, "w1": w["w1"].float(), "w3": w["w3"].float(), "w2": w["w2"].float()}, 4, 2).forward(x)
+
+
+def test_a_layers_passes_run_on_its_device(xm, monkeypatch):
+    """Every launch of a pass with the weights' device as the current one."""
+    from padding_free_expert_amd import layer
+    at = [0]
+
+    @contextlib.contextmanager
+    def enter(like):
+        assert like.shape == (64, 4)    # the gate's weights
+        at.append(1)
+        yield
+        at.pop()
+
+    Device(monkeypatch, LAYER + BLOCK8)
+    launches = []
+    for n in set(LAYER + BLOCK8) - {"xmoe_add_rmsnorm", "xmoe_add_rmsnorm_bwd"}:    # these see to it themselves
+        monkeypatch.setattr(layer, n, lambda *a, **kw: launches.append(at[-1]))
+    monkeypatch.setattr(layer, "_on_device", enter)
+    w, x = _weights()
+    block = layer.MoEBlock(w, 4, 2, balance_alpha=0.1)
+    block.forward(x)
+    block.backward(x)
+    layer.MoEBlock8(w, 4, 2).forward(x)
+    m = layer.PaddingFreeMoE(w, 4, 2, merge_shared=True)
+    m.forward(x)
+    m.backward(x)
+    assert launches and set(launches) == {1} and at == [0]
