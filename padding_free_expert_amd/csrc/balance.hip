@@ -13,7 +13,9 @@
 // Piece (chunk b, sequence s) has row b + s of the partial sums: chunks and
 // sequences both only go forward, so no two pieces share a row and the rows
 // number at most chunks + S.  A second kernel adds a sequence's rows in order and
-// writes counts and coef; a third adds its blocks' losses in order.  Nothing depends on the order in which blocks run.  S' comes from the
+// writes counts and coef; its last block to end, or of many blocks a third kernel,
+// adds the blocks' losses in order.  Nothing depends on the order in which blocks
+// run.  S' comes from the
 // counted tokens of every sequence, whose pieces are added side by side, since a
 // sequence may be masked over any number of them: 2^20 tokens of 16 experts in two
 // sequences 52 us, one of them masked or not (379 and 50 where a thread looked for
@@ -64,6 +66,7 @@ struct BalanceWs {
     int32_t *csum;    // [rows, E]
     int32_t *nsum;    // [rows]
     double *part_loss; // [S, blocks of experts]
+    int32_t *ticket;  // [1]
     int32_t *nseq;    // [S]; nullptr: the second kernel counts by itself
     size_t bytes;
 };
@@ -81,6 +84,7 @@ BalanceWs balance_ws(void *ws, int64_t T, int E, int S) {
     b.csum = reinterpret_cast<int32_t *>(take(rows * E * 4));
     b.nsum = reinterpret_cast<int32_t *>(take(rows * 4));
     b.part_loss = reinterpret_cast<double *>(take(static_cast<size_t>(S) * final_blocks(E) * 8));
+    b.ticket = reinterpret_cast<int32_t *>(take(4));
     b.nseq = counts_itself(T, S) ? nullptr : reinterpret_cast<int32_t *>(take(static_cast<size_t>(S) * 4));
     b.bytes = at;
     return b;
@@ -150,6 +154,7 @@ __global__ __launch_bounds__(64 * kWaves) void balance_part_kernel(const float *
     const int r = lane % LT, slot = wave * TPW + lane / LT;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
     const int64_t t1 = t0 + chunk < T ? t0 + chunk : T;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *ws.ticket = 0;
     auto ex = [&](int q) { return 4 * (r + LT * (q >> 2)) + (q & 3); };
     // the first step's logits are on their way during the search: the first piece
     // starts with the chunk unless the chunk starts in front of the first sequence
@@ -267,8 +272,9 @@ __global__ __launch_bounds__(256) void balance_count_kernel(int64_t T, const int
 // A block per sequence and 32 experts.  The rows' values are asked for first;
 // what the counts need (n_s, S') comes beside them.
 __global__ __launch_bounds__(1024) void balance_final_kernel(int64_t T, int E, int k, const int32_t *off, int S,
-                                                             int chunk, float alpha, BalanceWs ws, float *loss,
-                                                             int32_t *counts, float *coef) {
+                                                             int chunk, float alpha, BalanceWs ws, bool hand_over,
+                                                             float *loss, int32_t *counts, float *coef) {
+    __shared__ bool last;
     __shared__ double red[32];
     __shared__ int32_t wn[16], wsome[16];
     __shared__ double sp[kFinalExperts][33];
@@ -357,30 +363,48 @@ __global__ __launch_bounds__(1024) void balance_final_kernel(int64_t T, int E, i
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
         return v;
     };
-    if (threadIdx.x >= 64) return;
-    l = sum32(red[threadIdx.x % 32]);
-    if (threadIdx.x != 0) return;
-    if (gridDim.x == 1) *loss = static_cast<float>(l);
-    else ws.part_loss[blockIdx.x] = l;
+    if (threadIdx.x < 64) l = sum32(red[threadIdx.x % 32]);
+    if (gridDim.x == 1) {
+        if (threadIdx.x == 0) *loss = static_cast<float>(l);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        ws.part_loss[blockIdx.x] = l;
+        if (hand_over)
+            last = __hip_atomic_fetch_add(ws.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+                   static_cast<int>(gridDim.x) - 1;
+    }
+    if (!hand_over) return;
+    // The last block to come adds the blocks' losses in order; nobody waits for
+    // anybody.  Taking the ticket releases the block's loss and acquires those of the
+    // blocks before it, the barrier hands that on to the first wave.
+    __syncthreads();
+    if (!last || threadIdx.x >= 64) return;
+    l = 0.0;
+    if (threadIdx.x < 32)
+        for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += 32) l += ws.part_loss[i];
+    l = sum32(l);
+    if (threadIdx.x == 0) *loss = static_cast<float>(l);
 }
 
-// The blocks' losses, added in order.  A kernel of its own: the end of a kernel
-// orders its stores for the next one.  Handed to the last block to come by a
-// counter in memory they cost as much or more (release and acquire: 4096 tokens of
-// 64 experts 10.6 us against 10.9 here, 32768 of 160 in 24 sequences 19.3 against
-// 17.2, 32768 of 512 in 60 sequences 44 against 33).
+// The blocks' losses, added in order, where there are more blocks than this.  Each
+// release writes an XCD's L2 back and the blocks take the ticket one by one: 32768
+// tokens of 512 experts in 4, 8, 12 and 60 sequences (64, 128, 192, 960 blocks) 24.8,
+// 25.8, 30.1 and (relaxed) 44 us by the ticket, 24.2, 23.7, 26.0 and 33 with this kernel;
+// 4096 tokens of 64 experts (2 blocks) 10.2 and 10.9, and a launch less on the host.
+constexpr int64_t kHandOverBlocks = 64;
 __global__ __launch_bounds__(1024) void balance_loss_kernel(const double *__restrict__ part, int n,
                                                             float *__restrict__ loss) {
     __shared__ double s[16];
     double l = 0.0;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += blockDim.x) l += part[i];
+    for (int i = threadIdx.x; i < n; i += 1024) l += part[i];
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o, 64);
     if (threadIdx.x % 64 == 0) s[threadIdx.x / 64] = l;
     __syncthreads();
     if (threadIdx.x != 0) return;
-    for (int w = 1; w < static_cast<int>(blockDim.x / 64); ++w) l += s[w];
+    for (int w = 1; w < 16; ++w) l += s[w];
     *loss = static_cast<float>(l);
 }
 
@@ -453,30 +477,29 @@ hipError_t launch_balance_loss(const float *logits, const int32_t *ids, int64_t 
                                int32_t *counts, float *coef, void *ws, hipStream_t st) {
     const BalanceWs w = balance_ws(ws, T, E, S);
     const int chunk = chunk_tokens(T);
-    const unsigned blocks = static_cast<unsigned>((T + chunk - 1) / chunk);
+    // one block at least: it clears the ticket
+    const unsigned blocks = static_cast<unsigned>(std::max<int64_t>((T + chunk - 1) / chunk, 1));
 #define XMOE_BALANCE_PART(LT, QQ)                                                                                  \
     hipLaunchKernelGGL((balance_part_kernel<LT, QQ>), dim3(blocks), dim3(64 * kWaves), 0, st, logits, ids, T, E, k, \
                        seq_offsets, S, mask, chunk, w)
     const bool many = T >= kManyTokens && E > 32;
-    hipError_t e;
-    if (blocks > 0) {
-        if (many && E <= 64) XMOE_BALANCE_PART(8, 8);
-        else if (many && E <= 128) XMOE_BALANCE_PART(8, 16);
-        else XMOE_BALANCE_SHAPE(E, XMOE_BALANCE_PART);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
+    if (many && E <= 64) XMOE_BALANCE_PART(8, 8);
+    else if (many && E <= 128) XMOE_BALANCE_PART(8, 16);
+    else XMOE_BALANCE_SHAPE(E, XMOE_BALANCE_PART);
 #undef XMOE_BALANCE_PART
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     if (w.nseq) {
         hipLaunchKernelGGL(balance_count_kernel, dim3(static_cast<unsigned>(S)), dim3(256), 0, st, T, seq_offsets, chunk, w);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const int64_t final = static_cast<int64_t>(S) * final_blocks(E);
+    const bool hand_over = final <= kHandOverBlocks;
     hipLaunchKernelGGL(balance_final_kernel, dim3(static_cast<unsigned>(final)), dim3(1024), 0, st, T, E, k, seq_offsets,
-                       S, chunk, alpha, w, loss, counts, coef);
-    if (final > 1) {
+                       S, chunk, alpha, w, hand_over, loss, counts, coef);
+    if (!hand_over) {
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(final <= 64 ? 64 : 1024), 0, st, w.part_loss,
-                           static_cast<int>(final), loss);
+        hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(1024), 0, st, w.part_loss, static_cast<int>(final), loss);
     }
     return hipGetLastError();
 }
