@@ -623,7 +623,11 @@ xmoe_status xmoe_mx8_quantize_weights(const void *w, xmoe_dtype dtype, int32_t E
  * with their scales as xmoe_mx8_quantize_weights lays them out (from the
  * layer's [E,d,h] and [E,h,d]).  act [rows,h], act_scale [ceil(h/128),rows,4].
  * expert_offsets as xmoe_expert_ffn_up; rows outside every segment are left as
- * they were.  Deterministic.  A NaN in a row's block makes NaNs of that row.
+ * they were.  Deterministic: the same call gives the same bits.  Which kernel runs
+ * goes by rows, E and the widths; they add in another order and form silu with a
+ * division or a reciprocal, so that an element of a row's act next to a rounding
+ * boundary may be the neighbouring value in a batch of another size.  A NaN in a
+ * row's block makes NaNs of that row.
  * Limits: d, h multiples of 32, at most 65536; E <= 1024; rows * max(d, h, 512)
  * < 2^34; T * d < 2^31 with token_ids.
  */

@@ -15,15 +15,17 @@
 // number at most chunks + S.  A second kernel adds a sequence's rows in order and
 // writes counts and coef; its last block to end, or of many blocks a third kernel,
 // adds the blocks' losses in order.  Nothing depends on the order in which blocks
-// run.  S' comes from the
-// counted tokens of every sequence, whose pieces are added side by side, since a
-// sequence may be masked over any number of them: 2^20 tokens of 16 experts in two
-// sequences 52 us, one of them masked or not (379 and 50 where a thread looked for
-// a sequence's first counted piece).  The logits are read
-// once here, once in the backward, which writes the gradient.  Bound by latency:
-// 4096 tokens of 64 experts take 3.7 + 6.2 us and 3.4 us back, most of it launch,
-// first loads and the hand-over between compute units; 32768 of 160 experts in
-// 24 sequences (63 MB in all) 11.2 + 7.2 and 10.1 us.
+// run.  S' comes from the counted tokens of every sequence, whose pieces are added
+// side by side, since a sequence may be masked over any number of them: 2^20
+// tokens of 16 experts in two sequences 51 us, one of them masked or not (379 and
+// 50 where a thread looked for a sequence's first counted piece).
+//
+// The logits are read once here, once in the backward, which writes the gradient.
+// Bound by latency: 4096 tokens of 64 experts take 3.7 + 6.5 us and 3.6 us back,
+// the second kernel's two blocks a chain of loads that wait for each other
+// (offsets, counts, rows) and the ticket; 32768 of 160 experts in 24 sequences (63
+// MB in all) 11.2 + 5.6 + 1.8 and 11.5 us (logits out of memory; 10 where the
+// last-level cache holds them).
 #include <algorithm>
 
 #include "balance.hpp"
