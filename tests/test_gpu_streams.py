@@ -169,3 +169,53 @@ def test_two_callers_at_once(xm):
     for c, a in zip(callers, alone):
         for n, t in c.out.items():
             assert torch.equal(t, a[n]), n
+
+
+@pytest.mark.parametrize("S", [1, 3, 70])
+def test_workspaces_of_captured_calls_on_a_forked_stream(xm, S):
+    """Calls that allocate their workspaces, captured on a stream forked from the
+    capture's: every replay on new inputs has the bits of eager calls, with eager
+    work and synchronizations between the replays."""
+    T, d, E, k = 2500, 512, 160, 6
+    g = _gen(S)
+    off = None if S == 1 else torch.linspace(0, T - 3, S + 1, device="cuda").to(torch.int32)
+    gamma = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    s, dy = (torch.empty((T, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    rstd, logits = torch.empty(T, device="cuda"), torch.empty((T, E), device="cuda")
+    ids = torch.empty((T, k), dtype=torch.int32, device="cuda")
+
+    def fill():
+        s.copy_(torch.randn((T, d), generator=g, device="cuda"))
+        dy.copy_(torch.randn((T, d), generator=g, device="cuda"))
+        rstd.copy_(torch.rsqrt(s.float().square().mean(1) + EPS))
+        logits.copy_(torch.randn((T, E), generator=g, device="cuda"))
+        ids.copy_(torch.topk(logits, k, 1).indices)
+
+    def buffers():
+        return (torch.empty_like(s), torch.empty(d, device="cuda"), torch.empty(1, device="cuda"),
+                torch.empty((S, E), dtype=torch.int32, device="cuda"), torch.empty((S, E), device="cuda"))
+
+    def call(o, stream=None):
+        xm.xmoe_add_rmsnorm_bwd(dy, None, s, gamma, rstd, o[0], o[1], stream=stream)
+        xm.xmoe_balance_loss(logits, ids, 0.1, o[2], o[3], o[4], off, stream=stream)
+
+    fill()
+    got, want = buffers(), buffers()
+    call(got)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        call(got, side)
+        main.wait_stream(side)
+    for i in range(5):
+        fill()
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        call(want)
+        torch.cuda.synchronize()
+        for n, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), (i, n)
