@@ -639,6 +639,57 @@ xmoe_status xmoe_expert_ffn_down_mx8(const void *act, const void *act_scale, con
                                      const int32_t *expert_offsets, int32_t E, int64_t rows, int32_t d, int32_t h,
                                      void *ye, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The whole layer for a few tokens (0 <= T <= 64), forward only: gate, top-k,
+ * experts, shared experts and combine in one call, for the next tokens of a few
+ * sequences.  The weights that the tokens chose are read once; no Padding-Free
+ * Token buffer is built.
+ *   logits, topk_ids, topk_w : as xmoe_route
+ *   a[t,j] = silu(x[t] . w1[e]) * (x[t] . w3[e]),  e = topk_ids[t,j]
+ *   y[t]   = sum_j topk_w[t,j] * (a[t,j] . w2[e])  (+ the shared experts' FFN of x[t])
+ * fp32 sums; a is rounded once to the dtype, y once at the end (the experts'
+ * outputs are not rounded in between, as xmoe_expert_ffn_down does).  The sums run
+ * in another order than xmoe_route's and xmoe_expert_ffn_up's, so that results
+ * agree to rounding, and experts whose selection values differ by less than that
+ * may be chosen the other way round.  Whatever the logits hold, a token's ids are
+ * distinct and in [0, E); a NaN counts as the largest selection value.
+ * x, y [T,d]; wg [d,E]; w1, w3 [E,d,h]; w2 [E,h,d]; the shared experts side by
+ * side: s1, s3 [d,hs], s2 [hs,d], hs = 0: none (s1, s3, s2 are not read).
+ * topk_ids int32 [T,k], topk_w fp32 [T,k], logits fp32 [T,E] are outputs.
+ * workspace: device, 16-byte aligned, >= xmoe_layer_few_workspace_size bytes, no
+ * initialisation needed, dead after the call (calls that overlap need one each).
+ * Deterministic; a token's row depends on T only through the order of its sums.
+ * Limits: 1 <= k <= E <= 1024; d, h, hs multiples of 8, at most 65536; bf16 needs
+ * E % 8 == 0; d * max(h, hs, E) elements have less than 2^31 bytes.
+ */
+size_t xmoe_layer_few_workspace_size(int64_t T, int32_t d, int32_t E, int32_t k, int32_t h, int32_t hs,
+                                     xmoe_dtype dtype);
+xmoe_status xmoe_layer_few(const void *x, const void *wg, const void *w1, const void *w3, const void *w2,
+                           const void *s1, const void *s3, const void *s2, xmoe_dtype dtype, int64_t T, int32_t d,
+                           int32_t E, int32_t k, int32_t h, int32_t hs, float inv_temperature, const float *logit_bias,
+                           const float *select_bias, int32_t *topk_ids, float *topk_w, float *logits, void *y,
+                           void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * The same on 8-bit rows and weights (bf16 gate, x and y): the gate reads x, the
+ * experts xq with xscale (8-bit rows [T,d]), and a is held in 8 bits, quantized from
+ * fp32, as xmoe_expert_ffn_up_mx8 leaves it; products and their error as there.
+ * Weights as xmoe_mx8_quantize_weights lays them out; the shared experts as one
+ * expert of width hs.  d, h, hs multiples of 32; other limits as xmoe_layer_few, with
+ * one byte an element for the experts' matrices.  The structs are read during the call.
+ */
+typedef struct {
+    const void *w1, *w1_scale, *w3, *w3_scale;  /* [n, h, d]  and scales [n, ceil(d/128), h, 4] */
+    const void *w2, *w2_scale;                  /* [n, d, h]  and scales [n, ceil(h/128), d, 4] */
+} xmoe_mx8_ffn;
+
+size_t xmoe_layer_few_mx8_workspace_size(int64_t T, int32_t d, int32_t E, int32_t k, int32_t h, int32_t hs);
+xmoe_status xmoe_layer_few_mx8(const void *x, const void *xq, const void *xscale, const void *wg,
+                               const xmoe_mx8_ffn *routed, const xmoe_mx8_ffn *shared, int64_t T, int32_t d, int32_t E,
+                               int32_t k, int32_t h, int32_t hs, float inv_temperature, const float *logit_bias,
+                               const float *select_bias, int32_t *topk_ids, float *topk_w, float *logits, void *y,
+                               void *workspace, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

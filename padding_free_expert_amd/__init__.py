@@ -30,6 +30,7 @@ __all__ = [
     "xmoe_balance_loss", "xmoe_balance_loss_workspace_size", "xmoe_balance_loss_bwd", "xmoe_route_bwd_balance",
     "mx8_scale_shape", "xmoe_mx8_quantize", "xmoe_mx8_dequantize", "xmoe_mx8_quantize_weights",
     "xmoe_expert_ffn_up_mx8", "xmoe_expert_ffn_down_mx8",
+    "xmoe_layer_few", "xmoe_layer_few_workspace_size", "xmoe_layer_few_mx8", "xmoe_layer_few_mx8_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -125,6 +126,18 @@ _lib_mx8_qw = _sig("xmoe_mx8_quantize_weights", [_vp, ctypes.c_int, _i32, _i32, 
 _lib_up8 = _sig("xmoe_expert_ffn_up_mx8", [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp,
                                            _vp, _vp])
 _lib_down8 = _sig("xmoe_expert_ffn_down_mx8", [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp])
+
+
+class _CMx8Ffn(ctypes.Structure):
+    _fields_ = [("w1", _vp), ("w1_scale", _vp), ("w3", _vp), ("w3_scale", _vp), ("w2", _vp), ("w2_scale", _vp)]
+
+
+_lib_few_ws = _sig("xmoe_layer_few_workspace_size", [_i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_int], _sz)
+_lib_few = _sig("xmoe_layer_few", [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _i64, _i32, _i32, _i32, _i32,
+                                   _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
+_lib_few8_ws = _sig("xmoe_layer_few_mx8_workspace_size", [_i64, _i32, _i32, _i32, _i32, _i32], _sz)
+_lib_few8 = _sig("xmoe_layer_few_mx8", [_vp, _vp, _vp, _vp, ctypes.POINTER(_CMx8Ffn), ctypes.POINTER(_CMx8Ffn), _i64,
+                                        _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
 
 
 class XmoeError(RuntimeError):
@@ -817,3 +830,84 @@ def xmoe_expert_ffn_down_mx8(act, act_scale, w2, w2_scale, expert_offsets, ye, s
     with _on_device(act, act_scale, w2, w2_scale, expert_offsets, ye):
         _check(_lib_down8(_ptr(act), _ptr(act_scale), _ptr(w2), _ptr(w2_scale), _ptr(expert_offsets), E, rows, d, h,
                           _ptr(ye), _stream_on(stream, act)), "xmoe_expert_ffn_down_mx8")
+
+
+def xmoe_layer_few_workspace_size(T: int, d: int, E: int, k: int, h: int, hs: int, dtype) -> int:
+    return int(_lib_few_ws(T, d, E, k, h, hs, XMOE_BF16 if dtype == torch.bfloat16 else XMOE_F32))
+
+
+def xmoe_layer_few_mx8_workspace_size(T: int, d: int, E: int, k: int, h: int, hs: int) -> int:
+    return int(_lib_few8_ws(T, d, E, k, h, hs))
+
+
+def _few_routing(x, wg, k, topk_ids, topk_w, logits, y, logit_bias, select_bias):
+    T, d = x.shape
+    E = wg.shape[1]
+    _shape(wg, (d, E), "wg", x.dtype)
+    _shape(topk_ids, (T, k), "topk_ids", _I32)
+    _shape(topk_w, (T, k), "topk_w", _F32)
+    _shape(logits, (T, E), "logits", _F32)
+    _shape(y, (T, d), "y", x.dtype)
+    _shape(logit_bias, (E,), "logit_bias", _F32)
+    _shape(select_bias, (E,), "select_bias", _F32)
+    return T, d, E
+
+
+def xmoe_layer_few(x, wg, w1, w3, w2, k: int, topk_ids, topk_w, logits, y, inv_temperature: float = 1.0,
+                   logit_bias=None, select_bias=None, s1=None, s3=None, s2=None, workspace=None, stream=None):
+    """The whole layer for at most 64 tokens; topk_ids, topk_w, logits and y are
+    outputs.  s1, s3 [d, hs], s2 [hs, d]: the shared experts side by side (all or
+    none).  workspace: allocated here (torch) when None."""
+    T, d, E = _few_routing(x, wg, k, topk_ids, topk_w, logits, y, logit_bias, select_bias)
+    h = w1.shape[2]
+    _ffn_shapes(x.dtype, E, d, h, w1=w1, w3=w3, w2=w2)
+    if any(t is None for t in (s1, s3, s2)) and any(t is not None for t in (s1, s3, s2)):
+        raise ValueError("s1, s3 and s2: all of them, or none")
+    hs = 0
+    if s1 is not None:
+        hs = s1.shape[1]
+        _shape(s1, (d, hs), "s1", x.dtype)
+        _shape(s3, (d, hs), "s3", x.dtype)
+        _shape(s2, (hs, d), "s2", x.dtype)
+    dt = _dt(x)
+    workspace, nbytes = _workspace(workspace, int(_lib_few_ws(T, d, E, k, h, hs, dt)), x, stream)
+    with _on_device(x, wg, w1, w3, w2, s1, s3, s2, topk_ids, topk_w, logits, y, logit_bias, select_bias, workspace):
+        _check(_lib_few(_ptr(x), _ptr(wg), _ptr(w1), _ptr(w3), _ptr(w2), _ptr(s1), _ptr(s3), _ptr(s2), dt, T, d, E, k, h,
+                        hs, inv_temperature, _ptr(logit_bias), _ptr(select_bias), _ptr(topk_ids), _ptr(topk_w),
+                        _ptr(logits), _ptr(y), _ptr(workspace), nbytes, _stream_on(stream, x)), "xmoe_layer_few")
+
+
+def _mx8_ffn(w1, w3, w2, n: int, d: int, h: int, names=("w1", "w3", "w2")) -> _CMx8Ffn:
+    at = []
+    for (q, s), name, N, K in ((w1, names[0], h, d), (w3, names[1], h, d), (w2, names[2], d, h)):
+        _shape(q, (n, N, K), name, _F8)
+        _shape(s, (n,) + mx8_scale_shape(N, K), name + "_scale", _U8)
+        at += [_ptr(q), _ptr(s)]
+    return _CMx8Ffn(*at)
+
+
+def xmoe_layer_few_mx8(x, xq, xscale, wg, w1, w3, w2, k: int, topk_ids, topk_w, logits, y, inv_temperature: float = 1.0,
+                       logit_bias=None, select_bias=None, s1=None, s3=None, s2=None, workspace=None, stream=None):
+    """xmoe_layer_few with 8-bit rows and weights: each of w1, w3, w2 (and s1, s3, s2:
+    one expert of width hs) is the pair (q, scale) of xmoe_mx8_quantize_weights."""
+    T, d, E = _few_routing(x, wg, k, topk_ids, topk_w, logits, y, logit_bias, select_bias)
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x: dtype {x.dtype}, the call needs {torch.bfloat16}")
+    _shape(xq, (T, d), "xq", _F8)
+    _shape(xscale, mx8_scale_shape(T, d), "xscale", _U8)
+    h = w1[0].shape[1]
+    routed = _mx8_ffn(w1, w3, w2, E, d, h)
+    if any(t is None for t in (s1, s3, s2)) and any(t is not None for t in (s1, s3, s2)):
+        raise ValueError("s1, s3 and s2: all of them, or none")
+    hs, shared = 0, None
+    if s1 is not None:
+        hs = s1[0].shape[1]
+        shared = _mx8_ffn(s1, s3, s2, 1, d, hs, ("s1", "s3", "s2"))
+    workspace, nbytes = _workspace(workspace, int(_lib_few8_ws(T, d, E, k, h, hs)), x, stream)
+    more = () if s1 is None else (*s1, *s3, *s2)
+    with _on_device(x, xq, xscale, wg, *w1, *w3, *w2, *more, topk_ids, topk_w, logits, y, logit_bias, select_bias,
+                    workspace):
+        _check(_lib_few8(_ptr(x), _ptr(xq), _ptr(xscale), _ptr(wg), ctypes.byref(routed),
+                         None if shared is None else ctypes.byref(shared), T, d, E, k, h, hs, inv_temperature,
+                         _ptr(logit_bias), _ptr(select_bias), _ptr(topk_ids), _ptr(topk_w), _ptr(logits), _ptr(y),
+                         _ptr(workspace), nbytes, _stream_on(stream, x)), "xmoe_layer_few_mx8")
