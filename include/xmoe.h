@@ -690,6 +690,64 @@ xmoe_status xmoe_layer_few_mx8(const void *x, const void *xq, const void *xscale
                                const float *select_bias, int32_t *topk_ids, float *topk_w, float *logits, void *y,
                                void *workspace, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The expert FFN with its pre-activations kept in 8 bits, for training in less
+ * memory: the forward leaves [H1 | H3] as whole numbers, the backward reads them,
+ * rebuilds act and forms the routing weights' gradient without the experts'
+ * outputs.  Of a row only 2h bytes and h/16 scale bytes are kept, in place of
+ * h13, act and ye.
+ *
+ * 8-bit pre-activations: hq int8 [rows,2h], each value a whole number of -127..127
+ * times 2^(b - 127), b the scale byte of its block: 32 consecutive columns of H1 or
+ * of H3 (the last block of each may be shorter).  b is the least power of two that
+ * brings the block's largest magnitude to at most 127, not below 2^-127; elements
+ * are rounded to nearest even, once, from the fp32 sums.  A block of zeros has b =
+ * 127; one that holds an infinity or a NaN has b = 255 and stands for NaNs.  hscale
+ * is uint8 [2, ceil(h/128), rows, 4]: byte (half, g / 4, row, g % 4) belongs to
+ * columns [32 g, 32 g + 32) of that half (H1's, then H3's); bytes past h are 127.
+ *
+ * xmoe_expert_ffn_up_ckpt8: act as xmoe_expert_ffn_up / _up_gather write it, bit for
+ * bit (act itself is not formed from the 8 bits); H1, H3 -> hq, hscale.  token_ids
+ * DEVICE int32 [rows], or NULL: row r is x[r] (then T == rows).  Limits as those
+ * calls.  Rows outside every segment are left as they were.
+ */
+xmoe_status xmoe_expert_ffn_up_ckpt8(const void *x, const int32_t *token_ids, int64_t T, const void *w1,
+                                     const void *w3, xmoe_dtype dtype, const int32_t *expert_offsets, int32_t E,
+                                     int64_t rows, int32_t d, int32_t h, void *act, void *hq, void *hscale,
+                                     void *stream);
+
+/*
+ * The values of 8-bit pre-activations: h13 [rows,2h] (dtype), exact in bf16 too
+ * (seven bits and a power of two) where the dtype's exponent range holds them.
+ * rows * max(h / 4, 256) < 2^32.
+ */
+xmoe_status xmoe_ckpt8_dequantize(const void *hq, const void *hscale, xmoe_dtype dtype, int64_t rows, int32_t h,
+                                  void *h13, void *stream);
+
+/*
+ * Backward up to the pre-activations, H1 and H3 being the values that hq, hscale
+ * stand for:
+ *   dA[r]       = dy[token_ids[r]] . w2[e]^T                 (token_ids NULL: dy[r])
+ *   dH1, dH3    = row_weights[r] * dA[r] through the SwiGLU, as _dact -> dh13 [rows,2h]
+ *   act[r]      = row_weights[r] * silu(H1) * H3                       (act [rows,h])
+ *   dweights[i] = < dA[r], silu(H1) * H3 >,  r = slot_to_row[i]           (fp32 [rows])
+ * in fp32, each rounded once.  row_weights fp32 [rows] or NULL (all 1).  act carries
+ * the row's weight so that xmoe_expert_ffn_bwd_dw2 takes it with the rows of dy as
+ * they are (xmoe_dispatch of dy, or dy itself).  dweights NULL: not wanted; else
+ * slot_to_row DEVICE int32 [rows] (NULL: r = i), so that it is the routing weights'
+ * gradient [T,k] in the layer's order: the derivative of the layer's output at the
+ * kept pre-activations.  Slots whose row lies in no segment keep what they hold.
+ * workspace (with dweights): device, 16-byte aligned, >=
+ * xmoe_expert_ffn_bwd_dact_ckpt8_workspace_size bytes, no initialisation needed, dead
+ * after the call.  Limits as xmoe_expert_ffn_bwd_dact_gather.  Deterministic.
+ */
+size_t xmoe_expert_ffn_bwd_dact_ckpt8_workspace_size(int64_t rows, int32_t h);
+xmoe_status xmoe_expert_ffn_bwd_dact_ckpt8(const void *dy, const int32_t *token_ids, const float *row_weights,
+                                           int64_t T, const void *w2, const void *hq, const void *hscale,
+                                           xmoe_dtype dtype, const int32_t *expert_offsets, int32_t E, int64_t rows,
+                                           int32_t d, int32_t h, void *dh13, void *act, const int32_t *slot_to_row,
+                                           float *dweights, void *workspace, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -31,6 +31,8 @@ __all__ = [
     "mx8_scale_shape", "xmoe_mx8_quantize", "xmoe_mx8_dequantize", "xmoe_mx8_quantize_weights",
     "xmoe_expert_ffn_up_mx8", "xmoe_expert_ffn_down_mx8",
     "xmoe_layer_few", "xmoe_layer_few_workspace_size", "xmoe_layer_few_mx8", "xmoe_layer_few_mx8_workspace_size",
+    "ckpt8_scale_shape", "xmoe_expert_ffn_up_ckpt8", "xmoe_ckpt8_dequantize", "xmoe_expert_ffn_bwd_dact_ckpt8",
+    "xmoe_expert_ffn_bwd_dact_ckpt8_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -138,6 +140,13 @@ _lib_few = _sig("xmoe_layer_few", [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctype
 _lib_few8_ws = _sig("xmoe_layer_few_mx8_workspace_size", [_i64, _i32, _i32, _i32, _i32, _i32], _sz)
 _lib_few8 = _sig("xmoe_layer_few_mx8", [_vp, _vp, _vp, _vp, ctypes.POINTER(_CMx8Ffn), ctypes.POINTER(_CMx8Ffn), _i64,
                                         _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
+
+_lib_up_ck8 = _sig("xmoe_expert_ffn_up_ckpt8", [_vp, _vp, _i64, _vp, _vp, ctypes.c_int, _vp, _i32, _i64, _i32, _i32, _vp,
+                                                _vp, _vp, _vp])
+_lib_ck8_dq = _sig("xmoe_ckpt8_dequantize", [_vp, _vp, ctypes.c_int, _i64, _i32, _vp, _vp])
+_lib_dact_ck8_ws = _sig("xmoe_expert_ffn_bwd_dact_ckpt8_workspace_size", [_i64, _i32], _sz)
+_lib_dact_ck8 = _sig("xmoe_expert_ffn_bwd_dact_ckpt8", [_vp, _vp, _vp, _i64, _vp, _vp, _vp, ctypes.c_int, _vp, _i32, _i64,
+                                                        _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
 
 
 class XmoeError(RuntimeError):
@@ -911,3 +920,72 @@ def xmoe_layer_few_mx8(x, xq, xscale, wg, w1, w3, w2, k: int, topk_ids, topk_w, 
                          None if shared is None else ctypes.byref(shared), T, d, E, k, h, hs, inv_temperature,
                          _ptr(logit_bias), _ptr(select_bias), _ptr(topk_ids), _ptr(topk_w), _ptr(logits), _ptr(y),
                          _ptr(workspace), nbytes, _stream_on(stream, x)), "xmoe_layer_few_mx8")
+
+
+# ------------------------------- pre-activations kept in 8 bits
+
+def ckpt8_scale_shape(rows: int, h: int):
+    """Shape of the scale bytes of 8-bit pre-activations [rows, 2 h]."""
+    return (2, (h + 127) // 128, rows, 4)
+
+
+def _ckpt8(rows: int, h: int, hq, hscale) -> None:
+    _shape(hq, (rows, 2 * h), "hq", torch.int8)
+    _shape(hscale, ckpt8_scale_shape(rows, h), "hscale", _U8)
+
+
+def xmoe_expert_ffn_up_ckpt8(x, w1, w3, expert_offsets, act, hq, hscale, token_ids=None, stream=None):
+    """act [rows, h] as xmoe_expert_ffn_up (token_ids: _up_gather) and the
+    pre-activations in 8 bits: hq int8 [rows, 2 h], hscale ckpt8_scale_shape(rows, h)."""
+    T, d = x.shape
+    E, _, h = w1.shape
+    rows = T if token_ids is None else token_ids.shape[0]
+    _ffn_shapes(x.dtype, E, d, h, w1=w1, w3=w3, offsets=expert_offsets)
+    _shape(token_ids, (rows,), "token_ids", _I32)
+    _shape(act, (rows, h), "act", x.dtype)
+    _ckpt8(rows, h, hq, hscale)
+    with _on_device(x, token_ids, w1, w3, expert_offsets, act, hq, hscale):
+        _check(_lib_up_ck8(_ptr(x), _ptr(token_ids), T, _ptr(w1), _ptr(w3), _dt(x), _ptr(expert_offsets), E, rows, d, h,
+                           _ptr(act), _ptr(hq), _ptr(hscale), _stream_on(stream, x)), "xmoe_expert_ffn_up_ckpt8")
+
+
+def xmoe_ckpt8_dequantize(hq, hscale, h13, stream=None):
+    """The values [rows, 2 h] of 8-bit pre-activations, in h13's dtype."""
+    rows, h = h13.shape[0], h13.shape[1] // 2
+    _shape(h13, (rows, 2 * h), "h13")
+    _ckpt8(rows, h, hq, hscale)
+    with _on_device(hq, hscale, h13):
+        _check(_lib_ck8_dq(_ptr(hq), _ptr(hscale), _dt(h13), rows, h, _ptr(h13), _stream_on(stream, h13)),
+               "xmoe_ckpt8_dequantize")
+
+
+def xmoe_expert_ffn_bwd_dact_ckpt8_workspace_size(rows: int, h: int) -> int:
+    return int(_lib_dact_ck8_ws(rows, h))
+
+
+def xmoe_expert_ffn_bwd_dact_ckpt8(dy, w2, hq, hscale, expert_offsets, dh13, act, token_ids=None, row_weights=None,
+                                   slot_to_row=None, dweights=None, workspace=None, stream=None):
+    """dh13 [rows, 2 h] and act [rows, h] (times row_weights) from dy and the 8-bit
+    pre-activations; dweights (fp32, rows elements, or None): <dA, act> of the row of
+    each slot.  workspace: allocated here (torch) when None and dweights is wanted."""
+    T, d = dy.shape
+    rows, h = act.shape
+    E = w2.shape[0]
+    _ffn_shapes(dy.dtype, E, d, h, w2=w2, offsets=expert_offsets)
+    if token_ids is None:
+        _shape(dy, (rows, d), "dy", dy.dtype)
+    _shape(token_ids, (rows,), "token_ids", _I32)
+    _shape(row_weights, (rows,), "row_weights", _F32)
+    _shape(slot_to_row, (rows,), "slot_to_row", _I32)
+    _shape(dh13, (rows, 2 * h), "dh13", dy.dtype)
+    _shape(act, (rows, h), "act", dy.dtype)
+    _ckpt8(rows, h, hq, hscale)
+    nbytes = 0
+    if dweights is not None:
+        if dweights.numel() != rows or dweights.dtype != _F32:
+            raise ValueError(f"dweights: {rows} fp32 elements are needed")
+        workspace, nbytes = _workspace(workspace, int(_lib_dact_ck8_ws(rows, h)), dy, stream)
+    with _on_device(dy, w2, hq, hscale, expert_offsets, dh13, act, token_ids, row_weights, slot_to_row, dweights, workspace):
+        _check(_lib_dact_ck8(_ptr(dy), _ptr(token_ids), _ptr(row_weights), T, _ptr(w2), _ptr(hq), _ptr(hscale), _dt(dy),
+                             _ptr(expert_offsets), E, rows, d, h, _ptr(dh13), _ptr(act), _ptr(slot_to_row), _ptr(dweights),
+                             _ptr(workspace), nbytes, _stream_on(stream, dy)), "xmoe_expert_ffn_bwd_dact_ckpt8")

@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libxmoe.so")
 SOURCES = ["api.cpp", "api_block.cpp", "route.hip", "pft.hip", "rows.hip", "ffn.hip", "ep.hip", "norm.hip",
-           "balance.hip", "mx8.hip", "api_few.cpp", "few.hip"]
+           "balance.hip", "mx8.hip", "api_few.cpp", "few.hip", "api_ckpt8.cpp"]
 
 
 def _hipcc() -> str:

@@ -189,6 +189,129 @@ hipError_t launch_ffn_bwd_dact(int dt, const void *dye, const int32_t *row_map, 
     return err;
 }
 
+// ------------------------------------------- pre-activations kept in 8 bits
+
+// launch_ffn_up whose epilogue leaves H1 and H3 in 8 bits (ckpt8.hpp)
+hipError_t launch_ffn_up_ckpt8(int dt, const void *xs, const int32_t *row_map, int64_t map_rows, const void *w1,
+                               const void *w3, const int32_t *offsets, int E, int64_t rows, int d, int h, void *act,
+                               void *hq, void *hscale, hipStream_t s) {
+    GemmArgs p = rows_args(offsets, E, rows);
+    p.a_map = row_map;
+    p.a_map_rows = map_rows;
+    p.N = h;
+    p.K = d;
+    p.A0 = xs;
+    p.lda = d;
+    p.B0 = w1;
+    p.Bx = w3;
+    p.ldb = h;
+    p.b_gstride = static_cast<int64_t>(d) * h;
+    p.C0 = act;
+    p.ldc = h;
+    p.aux_out = hq;
+    p.ld_aux = 2 * static_cast<int64_t>(h);
+    p.hoff = h;
+    p.ck_scale = static_cast<uint8_t *>(hscale);
+    if (dt != kBF16) return launch_gemm_f32<2, true, false, EPI_SWIGLU_CK8>(p, s);
+    // tiles by launch_ffn_up's rules
+    if (large_tiles(rows, E, h, 128))
+        return launch_gemm_dma<256, 128, 32, 4, 2, 2, true, false, 4, EPI_SWIGLU_CK8, bf16_t, 1>(p, s);
+    if (h % 256 == 0 && rows / (E > 0 ? E : 1) < 1024)
+        return launch_gemm_dma<128, 256, 32, 2, 4, 2, true, false, 3, EPI_SWIGLU_CK8, bf16_t, 1>(p, s);
+    return launch_gemm_dma<128, 128, 32, 2, 2, 2, true, false, 3, EPI_SWIGLU_CK8, bf16_t, 2>(p, s);
+}
+
+namespace {
+
+// dweights of slot i (row slot_to_row[i], or i): the column tiles' parts in order.
+// Rows in no segment keep what they hold.
+__global__ __launch_bounds__(256) void ckpt8_dots_kernel(const float *__restrict__ part, int tiles, int64_t rows,
+                                                         const int32_t *__restrict__ offsets, int E,
+                                                         const int32_t *__restrict__ slot_to_row,
+                                                         float *__restrict__ out) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= rows) return;
+    const int64_t r = slot_to_row ? slot_to_row[i] : i;
+    if (r < max(offsets[0], 0) || r >= min(static_cast<int64_t>(offsets[E]), rows)) return;
+    float v = part[r];
+    for (int t = 1; t < tiles; ++t) v += part[static_cast<int64_t>(t) * rows + r];
+    out[i] = v;
+}
+
+// hq, hscale -> [H1 | H3]: a thread for eight columns of a row
+template <typename T>
+__global__ __launch_bounds__(256) void ckpt8_dequantize_kernel(const uint8_t *__restrict__ hq,
+                                                               const uint8_t *__restrict__ hs, int64_t rows, int h,
+                                                               T *__restrict__ out) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int per = h / 4;  // of both halves
+    const int64_t r = i / per;
+    if (r >= rows) return;
+    const int c = static_cast<int>(i - r * per) * 8, b = c >= h ? 1 : 0, n = c - b * h;
+    const int groups = (h + 127) / 128;
+    const float s = ck8_scale(hs[((static_cast<int64_t>(b) * groups + n / 128) * rows + r) * 4 + n % 128 / 32]);
+    const uint2 v = *reinterpret_cast<const uint2 *>(hq + r * 2 * h + c);
+    float f[8];
+    ck8_unpack4(v.x, s, f);
+    ck8_unpack4(v.y, s, f + 4);
+    uint4 *dst = reinterpret_cast<uint4 *>(out + r * 2 * h + c);
+#pragma unroll
+    for (int j = 0; j < 8 / Elem<T>::kVec; ++j) dst[j] = Elem<T>::pack(f + j * Elem<T>::kVec);
+}
+
+}  // namespace
+
+hipError_t launch_ckpt8_dequantize(int dt, const void *hq, const void *hscale, int64_t rows, int h, void *out,
+                                   hipStream_t s) {
+    if (rows <= 0) return hipSuccess;
+    const dim3 grid(static_cast<unsigned>((rows * (h / 4) + 255) / 256));
+    const uint8_t *q = static_cast<const uint8_t *>(hq), *sc = static_cast<const uint8_t *>(hscale);
+    if (dt == kBF16)
+        hipLaunchKernelGGL((ckpt8_dequantize_kernel<bf16_t>), grid, dim3(256), 0, s, q, sc, rows, h, static_cast<bf16_t *>(out));
+    else
+        hipLaunchKernelGGL((ckpt8_dequantize_kernel<float>), grid, dim3(256), 0, s, q, sc, rows, h, static_cast<float *>(out));
+    return hipGetLastError();
+}
+
+// launch_ffn_bwd_dact with H1 and H3 in 8 bits; also act (times the row's scale) and, in
+// dweights, <dA, act> of each row before that scale.  ws: [column tiles, rows] floats
+// (64 columns a tile at least).
+hipError_t launch_ffn_bwd_dact_ckpt8(int dt, const void *dye, const int32_t *row_map, int64_t map_rows,
+                                     const float *row_scale, const void *w2, const void *hq, const void *hscale,
+                                     const int32_t *offsets, int E, int64_t rows, int d, int h, void *dh13, void *act,
+                                     const int32_t *slot_to_row, float *dweights, void *ws, hipStream_t s) {
+    if (rows <= 0) return hipSuccess;
+    GemmArgs p = rows_args(offsets, E, rows);
+    p.N = h;
+    p.K = d;
+    p.A0 = dye;
+    p.a_map = row_map;
+    p.a_map_rows = map_rows;
+    p.row_scale = row_scale;
+    p.lda = d;
+    p.B0 = w2;
+    p.ldb = d;
+    p.b_gstride = static_cast<int64_t>(d) * h;
+    p.C0 = dh13;
+    p.ldc = 2 * static_cast<int64_t>(h);
+    p.aux = hq;
+    p.ld_aux = 2 * static_cast<int64_t>(h);
+    p.hoff = h;
+    p.ck_scale = static_cast<uint8_t *>(const_cast<void *>(hscale));
+    p.ck_act = act;
+    p.ck_dots = dweights ? static_cast<float *>(ws) : nullptr;
+    // tiles by launch_ffn_bwd_dact's rule
+    const int bn = dt == kBF16 ? 256 : 64;
+    hipError_t err = dt != kBF16 ? launch_gemm_f32<1, true, true, EPI_SWIGLU_BWD_CK8>(p, s)
+                     : large_tiles_filled(rows, E, h, 256)
+                         ? launch_gemm_dma<256, 256, 32, 4, 2, 1, true, true, 4, EPI_SWIGLU_BWD_CK8, bf16_t, 1>(p, s)
+                         : launch_gemm_dma<128, 256, 32, 2, 2, 1, true, true, 3, EPI_SWIGLU_BWD_CK8, bf16_t, 2>(p, s);
+    if (err != hipSuccess || !dweights) return err;
+    hipLaunchKernelGGL(ckpt8_dots_kernel, dim3(static_cast<unsigned>((rows + 255) / 256)), dim3(256), 0, s, p.ck_dots,
+                       (h + bn - 1) / bn, rows, offsets, E, slot_to_row, dweights);
+    return hipGetLastError();
+}
+
 // dxs = dH1 . W1[e]^T + dH3 . W3[e]^T
 hipError_t launch_ffn_bwd_dx(int dt, const void *dh13, const void *w1, const void *w3, const int32_t *offsets, int E,
                              int64_t rows, int d, int h, void *dxs, bool accumulate, hipStream_t s) {

@@ -25,12 +25,14 @@
 #include <climits>
 #include <type_traits>
 
+#include "ckpt8.hpp"
 #include "common.hpp"
 
 namespace xmoe {
 
 enum { GM_ROWS = 0, GM_KSPLIT = 1 };
-enum { EPI_STORE = 0, EPI_ACCUM = 1, EPI_SWIGLU = 2, EPI_SWIGLU_BWD = 3, EPI_ROUTER = 4 };
+enum { EPI_STORE = 0, EPI_ACCUM = 1, EPI_SWIGLU = 2, EPI_SWIGLU_BWD = 3, EPI_ROUTER = 4, EPI_SWIGLU_CK8 = 5,
+       EPI_SWIGLU_BWD_CK8 = 6 };
 
 struct GemmArgs {
     int group_mode;
@@ -53,6 +55,12 @@ struct GemmArgs {
     void *aux_out;           // EPI_SWIGLU: [H1|H3] to save (optional)
     int64_t ld_aux;
     int hoff;                // column offset of the H3 half in [H1|H3]
+    // EPI_SWIGLU_CK8 (writes) and EPI_SWIGLU_BWD_CK8 (reads): [H1|H3] in 8 bits
+    // (ckpt8.hpp) at aux_out / aux, rows of 2N bytes, with these scales
+    // [2, ceil(N / 128), extent, 4]
+    uint8_t *ck_scale;
+    void *ck_act;            // EPI_SWIGLU_BWD_CK8: row_scale * silu(H1) * H3 [extent, N]
+    float *ck_dots;          // ... [column tiles, extent] parts of <dA, silu(H1) * H3> (optional)
     float scale;             // EPI_ROUTER
     const float *col_bias;   // EPI_ROUTER (optional)
     // GM_ROWS with a k-contiguous A (bf16 pipelined and fp32 kernels only):
@@ -660,6 +668,242 @@ __device__ __forceinline__ void gemm_epilogue(const GemmArgs &p, const Tile &t, 
         }
         return;
     }
+    if constexpr (EPI == EPI_SWIGLU_CK8) {
+        // act as above; H1 and H3 in 8 bits.  A lane holds 16 of the 32 columns of
+        // product (i, j) for its row, lane ^ 32 the others: a scale block is one
+        // product's row, and its columns past N are zeros, which change nothing.
+        constexpr int LDC = BN + 8, LDQ = BN + 8;
+        constexpr int kPass = BM * LDC * 2 <= RING ? 1 : WGM;
+        constexpr int RP = BM / kPass;
+        static_assert(NB == 2 && RP * LDC * 2 <= RING, "output tile must fit the ring");
+        typedef __bf16 bf4_t __attribute__((ext_vector_type(4)));
+        typedef float f4_t __attribute__((ext_vector_type(4)));
+        __bf16 *cs = reinterpret_cast<__bf16 *>(smem);
+        const int groups = (p.N + 127) / 128;
+        __syncthreads();  // every wave is done with the ring
+        for (int o = 0; o < 3; ++o) {
+            uint8_t *const dq = static_cast<uint8_t *>(p.aux_out) + q.crow * p.ld_aux + (o == 2 ? p.hoff : 0);
+            __bf16 *const da = static_cast<__bf16 *>(p.C0) + q.crow * p.ldc;
+            for (int pass = 0; pass < kPass; ++pass) {
+                if (kPass == 1 || wm == pass) {
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) {
+                        const int row = (kPass == 1 ? wm * WTM : 0) + i * 32 + (lane & 31);
+                        uint32_t bytes = 0u;
+#pragma unroll
+                        for (int j = 0; j < TN; ++j) {
+                            float inv = 1.0f;
+                            if (o != 0) {
+                                uint32_t a = 0u;
+#pragma unroll
+                                for (int r = 0; r < 16; ++r)
+                                    a = max(a, __float_as_uint(acc[o == 2][i][j][r]) & 0x7fffffffu);
+                                a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), 32, 64)));
+                                const uint32_t b = ck8_scale_byte(a);
+                                bytes |= b << (8 * j);
+                                inv = ck8_inv_scale(b);
+                            }
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const int col = wn * WTN + j * 32 + 8 * g + 4 * (lane >> 5);
+                                if (o == 0) {
+                                    f4_t v;
+#pragma unroll
+                                    for (int r = 0; r < 4; ++r) {
+                                        const float a = acc[0][i][j][4 * g + r], b = acc[1][i][j][4 * g + r];
+                                        v[r] = a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)) * b;
+                                    }
+                                    *reinterpret_cast<bf4_t *>(cs + row * LDC + col) = __builtin_convertvector(v, bf4_t);
+                                } else {
+                                    const f32x16_t &v = acc[o == 2][i][j];
+                                    *reinterpret_cast<uint32_t *>(smem + row * LDQ + col) =
+                                        ck8_pack4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3], inv);
+                                }
+                            }
+                        }
+                        const int m = m_lane + i * 32, n = n0 + wn * WTN;
+                        if (o != 0 && lane < 32 && m < t.Mg && n / 128 < groups) {
+                            uint8_t *const s = p.ck_scale +
+                                               ((static_cast<int64_t>(o - 1) * groups + n / 128) * p.extent + q.crow + m) * 4 +
+                                               n % 128 / 32;
+                            if constexpr (TN == 4) *reinterpret_cast<uint32_t *>(s) = bytes;
+                            else *reinterpret_cast<uint16_t *>(s) = static_cast<uint16_t>(bytes);
+                        }
+                    }
+                }
+                static_assert(TN == 2 || TN == 4, "two or four scale bytes a wave and row");
+                __syncthreads();
+                // a row's values leave in 16-byte chunks, its bytes in 8-byte ones (h is a multiple of 8)
+#pragma unroll 4
+                for (int c = threadIdx.x; c < RP * BN / 8; c += NT) {
+                    const int row = c / (BN / 8), c8 = c % (BN / 8);
+                    const int m = m0 + pass * RP + row, n = n0 + 8 * c8;
+                    if (m < t.Mg && n < p.N) {
+                        if (o == 0)
+                            *reinterpret_cast<uint4 *>(da + m * p.ldc + n) =
+                                *reinterpret_cast<const uint4 *>(cs + row * LDC + 8 * c8);
+                        else
+                            *reinterpret_cast<uint2 *>(dq + m * p.ld_aux + n) =
+                                *reinterpret_cast<const uint2 *>(smem + row * LDQ + 8 * c8);
+                    }
+                }
+                if (o + 1 < 3 || pass + 1 < kPass) __syncthreads();
+            }
+        }
+        return;
+    }
+    if constexpr (EPI == EPI_SWIGLU_BWD_CK8) {
+        // H1 and H3 come as bytes by LDS DMA (both tiles of the block at once: they
+        // fit the ring), each lane takes those of its accumulators' places into
+        // registers and turns dA in place into dH1, dH3 and act, which leave through
+        // the ring as in the store epilogue.  16-byte chunk c of tile row r sits at
+        // chunk c ^ (r % 16).
+        constexpr int kCpr = BN / 16;  // chunks a row
+        static_assert(NB == 1 && kCpr == 16, "256 columns");
+        static_assert(2 * BM * BN <= RING, "both tiles of bytes must fit the ring");
+        constexpr int kBlk = BM * BN / 1024;  // 1 KiB loads per tile
+        static_assert(kBlk % NW == 0, "whole loads per wave");
+        constexpr int LDC = BN + 8;
+        constexpr int kPass = BM * LDC * 2 <= RING ? 1 : WGM;
+        constexpr int RP = BM / kPass;
+        static_assert(RP * LDC * 2 <= RING && WGN * BM * 4 <= RING, "output tile must fit the ring");
+        typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
+        typedef float f2_t __attribute__((ext_vector_type(2)));
+        const int groups = (p.N + 127) / 128;
+        const __amdgpu_buffer_rsrc_t raux = make_rsrc(static_cast<const uint8_t *>(p.aux) + (q.crow + m0) * p.ld_aux,
+                                                      static_cast<int64_t>(t.Mg - m0) * p.ld_aux);
+        __syncthreads();  // every wave is done with the ring
+#pragma unroll
+        for (int x = 0; x < kBlk / NW; ++x) {
+            const int blk = x * NW + wave;
+            const int o = blk * 1024 + lane * 16;
+            const int row = o / BN, c = ((o % BN) / 16) ^ (row & 15);
+            const int col = n0 + 16 * c;
+            const int off = static_cast<int>(row * p.ld_aux + col);
+            lds_dma16(raux, col < p.N ? off : kOob, sbase + blk * 1024);
+            lds_dma16(raux, col < p.N ? off + p.hoff : kOob, sbase + BM * BN + blk * 1024);
+        }
+        // scales of the lane's rows: dword (row, 128 columns) and the row's weight
+        float rsc[TM], dot[TM];
+        uint32_t sc[2][TM][WTN / 128];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int m = m_lane + i * 32;
+            rsc[i] = p.row_scale && m < t.Mg ? p.row_scale[q.crow + m] : 1.0f;
+            dot[i] = 0.0f;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int y = 0; y < WTN / 128; ++y) {
+                    const int gr = (n0 + wn * WTN) / 128 + y;
+                    sc[b][i][y] = m < t.Mg && gr < groups
+                                      ? *reinterpret_cast<const uint32_t *>(
+                                            p.ck_scale + ((static_cast<int64_t>(b) * groups + gr) * p.extent + q.crow + m) * 4)
+                                      : 0x7f7f7f7fu;
+                }
+        }
+        wait_vmem<0>();
+        __syncthreads();
+        // packed here and now: left to its use behind the barrier, what a pair is made
+        // of would be kept instead, more than the registers hold
+        auto pack2 = [](float lo, float hi) {
+            const f2_t v = {lo, hi};
+            uint32_t u = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf2_t));
+            asm volatile("" : "+v"(u));
+            return u;
+        };
+        uint32_t act[TM][TN][4][2];  // bf16 pairs
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const float s1 = ck8_scale((sc[0][i][j / 4] >> (8 * (j % 4))) & 255u);
+                const float s3 = ck8_scale((sc[1][i][j / 4] >> (8 * (j % 4))) & 255u);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    // four values at a time: spread over more of them, the values between
+                    // would not fit the registers
+                    __builtin_amdgcn_sched_barrier(0);
+                    float a1[4], a3[4], g1[4], g3[4], ac[4];
+                    const int row = wm * WTM + i * 32 + (lane & 31);
+                    const int col = wn * WTN + j * 32 + 8 * g + 4 * (lane >> 5);
+                    const int at = row * BN + 16 * ((col >> 4) ^ (row & 15)) + (col & 15);
+                    ck8_unpack4(*reinterpret_cast<const uint32_t *>(smem + at), s1, a1);
+                    ck8_unpack4(*reinterpret_cast<const uint32_t *>(smem + BM * BN + at), s3, a3);
+                    float part = 0.0f;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float v = acc[0][i][j][4 * g + r];
+                        const float sg = __builtin_amdgcn_rcpf(1.0f + __expf(-a1[r]));
+                        const float si = a1[r] * sg, va = v * rsc[i];
+                        ac[r] = si * a3[r];
+                        part = __builtin_fmaf(v, ac[r], part);
+                        ac[r] *= rsc[i];
+                        g1[r] = va * a3[r] * sg * (1.0f + a1[r] * (1.0f - sg));
+                        g3[r] = va * si;
+                    }
+                    // columns past N hold other bytes
+                    if (n_lane + j * 32 + 8 * g < p.N) dot[i] += part;
+                    asm volatile("" : "+v"(dot[i]));  // as pack2
+                    acc[0][i][j][4 * g] = __uint_as_float(pack2(g1[0], g1[1]));
+                    acc[0][i][j][4 * g + 1] = __uint_as_float(pack2(g1[2], g1[3]));
+                    acc[0][i][j][4 * g + 2] = __uint_as_float(pack2(g3[0], g3[1]));
+                    acc[0][i][j][4 * g + 3] = __uint_as_float(pack2(g3[2], g3[3]));
+                    act[i][j][g][0] = pack2(ac[0], ac[1]);
+                    act[i][j][g][1] = pack2(ac[2], ac[3]);
+                }
+            }
+        __syncthreads();  // the ring is free again
+        if (p.ck_dots) {
+            float *const ds = reinterpret_cast<float *>(smem);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const float v = dot[i] + __shfl_xor(dot[i], 32, 64);
+                if (lane < 32) ds[wn * BM + wm * WTM + i * 32 + lane] = v;
+            }
+            __syncthreads();
+            for (int r = threadIdx.x; r < BM; r += NT) {
+                float v = ds[r];
+#pragma unroll
+                for (int w = 1; w < WGN; ++w) v += ds[w * BM + r];
+                if (m0 + r < t.Mg) p.ck_dots[static_cast<int64_t>(t.nt) * p.extent + q.crow + m0 + r] = v;
+            }
+            __syncthreads();
+        }
+        __bf16 *const cs = reinterpret_cast<__bf16 *>(smem);
+        for (int o = 0; o < 3; ++o) {
+            const int64_t ld = o == 2 ? p.N : p.ldc;
+            __bf16 *const dst = static_cast<__bf16 *>(o == 2 ? p.ck_act : p.C0) + q.crow * ld + (o == 1 ? p.hoff : 0);
+            for (int pass = 0; pass < kPass; ++pass) {
+                if (kPass == 1 || wm == pass) {
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int j = 0; j < TN; ++j)
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const int row = (kPass == 1 ? wm * WTM : 0) + i * 32 + (lane & 31);
+                                const int col = wn * WTN + j * 32 + 8 * g + 4 * (lane >> 5);
+                                const f32x16_t &v = acc[0][i][j];
+                                *reinterpret_cast<uint2 *>(cs + row * LDC + col) =
+                                    o == 2 ? make_uint2(act[i][j][g][0], act[i][j][g][1])
+                                           : make_uint2(__float_as_uint(o ? v[4 * g + 2] : v[4 * g]),
+                                                        __float_as_uint(o ? v[4 * g + 3] : v[4 * g + 1]));
+                            }
+                }
+                __syncthreads();
+#pragma unroll 4
+                for (int c = threadIdx.x; c < RP * BN / 8; c += NT) {
+                    const int row = c / (BN / 8), c8 = c % (BN / 8);
+                    const int m = m0 + pass * RP + row, n = n0 + 8 * c8;
+                    if (m < t.Mg && n < p.N)
+                        *reinterpret_cast<uint4 *>(dst + m * ld + n) = *reinterpret_cast<const uint4 *>(cs + row * LDC + 8 * c8);
+                }
+                if (o + 1 < 3 || pass + 1 < kPass) __syncthreads();
+            }
+        }
+        return;
+    }
     if constexpr (std::is_same<OutT, bf16_t>::value && (EPI == EPI_SWIGLU_BWD || EPI == EPI_ACCUM)) {
         // Staged read-modify-write epilogue, one pass of rows at a time: the
         // tiles the epilogue reads (SwiGLU backward: the saved H1 and H3;
@@ -784,7 +1028,7 @@ __device__ __forceinline__ void gemm_epilogue(const GemmArgs &p, const Tile &t, 
                     v0[r] = acc[0][i][j][4 * g + r];
                     v1[r] = acc[NB - 1][i][j][4 * g + r];
                 }
-                epilogue4<EPI, OutT>(p, q.crow, q.coff, m, n, v0, v1);
+                if constexpr (EPI != EPI_SWIGLU_CK8 && EPI != EPI_SWIGLU_BWD_CK8) epilogue4<EPI, OutT>(p, q.crow, q.coff, m, n, v0, v1);
             }
     }
 }
@@ -1169,6 +1413,75 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs p) {
             }
             __syncthreads();
         }
+    }
+    if constexpr (EPI == EPI_SWIGLU_CK8 || EPI == EPI_SWIGLU_BWD_CK8) {
+        // a thread's four columns lie in one block of 32, the eight threads tx ^ 0..7 hold it
+        const int groups = (p.N + 127) / 128, n = n0 + tx * 4, blk = n / 32;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = m0 + ty * 4 + i;
+            const int64_t row = q.crow + m;
+            const bool live = m < t.Mg && n < p.N;
+            uint8_t *const sc = p.ck_scale + (static_cast<int64_t>(blk / 4) * p.extent + row) * 4 + blk % 4;
+            const int64_t half = static_cast<int64_t>(groups) * p.extent * 4;
+            if constexpr (EPI == EPI_SWIGLU_CK8) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t a = 0u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a = max(a, __float_as_uint(acc[b * (NB - 1)][i][j]) & 0x7fffffffu);
+#pragma unroll
+                    for (int off = 1; off < 8; off <<= 1)
+                        a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), off, 64)));
+                    const uint32_t byte = ck8_scale_byte(a);
+                    const float *v = acc[b * (NB - 1)][i];
+                    if (live)
+                        *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.aux_out) + row * p.ld_aux + b * p.hoff + n) =
+                            ck8_pack4(v[0], v[1], v[2], v[3], ck8_inv_scale(byte));
+                    // blocks behind N in the last group too: their values are zeros; a
+                    // last tile in the group's first half fills the second
+                    if (m < t.Mg && tx % 8 == 0) {
+                        sc[b * half] = static_cast<uint8_t>(byte);
+                        if (n0 + BN >= p.N && blk % 4 < 2) sc[b * half + 2] = 127;
+                    }
+                }
+                if (live) {
+                    float v[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = silu_f(acc[0][i][j]) * acc[NB - 1][i][j];
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.C0) + row * p.ldc + n) = make_float4(v[0], v[1], v[2], v[3]);
+                }
+            } else {
+                float dot = 0.0f;
+                if (live) {
+                    const uint8_t *const h = static_cast<const uint8_t *>(p.aux) + row * p.ld_aux + n;
+                    const float rs = p.row_scale ? p.row_scale[row] : 1.0f;
+                    float a1[4], a3[4], g1[4], g3[4], ac[4];
+                    ck8_unpack4(*reinterpret_cast<const uint32_t *>(h), ck8_scale(sc[0]), a1);
+                    ck8_unpack4(*reinterpret_cast<const uint32_t *>(h + p.hoff), ck8_scale(sc[half]), a3);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float v = acc[0][i][j], sg = 1.0f / (1.0f + __expf(-a1[j])), si = a1[j] * sg;
+                        ac[j] = si * a3[j];
+                        dot = __builtin_fmaf(v, ac[j], dot);
+                        ac[j] *= rs;
+                        g1[j] = v * rs * a3[j] * sg * (1.0f + a1[j] * (1.0f - sg));
+                        g3[j] = v * rs * si;
+                    }
+                    float *const o = static_cast<float *>(p.C0) + row * p.ldc + n;
+                    *reinterpret_cast<float4 *>(o) = make_float4(g1[0], g1[1], g1[2], g1[3]);
+                    *reinterpret_cast<float4 *>(o + p.hoff) = make_float4(g3[0], g3[1], g3[2], g3[3]);
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.ck_act) + row * p.N + n) =
+                        make_float4(ac[0], ac[1], ac[2], ac[3]);
+                }
+                if (p.ck_dots) {
+#pragma unroll
+                    for (int off = 1; off < 16; off <<= 1) dot += __shfl_xor(dot, off, 64);
+                    if (tx == 0 && m < t.Mg) p.ck_dots[static_cast<int64_t>(t.nt) * p.extent + row] = dot;
+                }
+            }
+        }
+        return;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)

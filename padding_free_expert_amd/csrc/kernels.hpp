@@ -140,4 +140,16 @@ hipError_t launch_ffn_up_mx8(const void *xq, const void *xscale, const int32_t *
 hipError_t launch_ffn_down_mx8(const void *act, const void *act_scale, const void *w2, const void *w2s,
                                const int32_t *offsets, int E, int64_t rows, int d, int h, void *ye, hipStream_t s);
 
+// the expert FFN with its pre-activations kept in 8 bits (ckpt8.hpp); row_map and
+// row_scale may be nullptr; slot_to_row may be (dweights by row), dweights too
+hipError_t launch_ffn_up_ckpt8(int dt, const void *xs, const int32_t *row_map, int64_t map_rows, const void *w1,
+                               const void *w3, const int32_t *offsets, int E, int64_t rows, int d, int h, void *act,
+                               void *hq, void *hscale, hipStream_t s);
+hipError_t launch_ckpt8_dequantize(int dt, const void *hq, const void *hscale, int64_t rows, int h, void *out,
+                                   hipStream_t s);
+hipError_t launch_ffn_bwd_dact_ckpt8(int dt, const void *dye, const int32_t *row_map, int64_t map_rows,
+                                     const float *row_scale, const void *w2, const void *hq, const void *hscale,
+                                     const int32_t *offsets, int E, int64_t rows, int d, int h, void *dh13, void *act,
+                                     const int32_t *slot_to_row, float *dweights, void *ws, hipStream_t s);
+
 }  // namespace xmoe

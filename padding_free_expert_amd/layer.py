@@ -13,14 +13,16 @@ from typing import Dict
 
 import torch
 
-from . import (PFT, _on_device, mx8_scale_shape, xmoe_add_rmsnorm, xmoe_add_rmsnorm_bwd, xmoe_add_rmsnorm_bwd_workspace_size,
-               xmoe_balance_loss, xmoe_balance_loss_workspace_size, xmoe_build_pft, xmoe_build_pft_shared,
-               xmoe_build_pft_workspace_size, xmoe_combine,
-               xmoe_combine_bwd, xmoe_dispatch_bwd, xmoe_expert_ffn_bwd,
-               xmoe_expert_ffn_bwd_dact_gather, xmoe_expert_ffn_bwd_dw13_gather, xmoe_expert_ffn_bwd_dw2, xmoe_expert_ffn_bwd_dx,
-               xmoe_expert_ffn_down, xmoe_expert_ffn_down_mx8, xmoe_expert_ffn_up, xmoe_expert_ffn_up_gather,
-               xmoe_expert_ffn_up_mx8, xmoe_mx8_quantize_weights, xmoe_route, xmoe_route_bwd, xmoe_route_bwd_balance,
-               xmoe_route_bwd_workspace_size, xmoe_route_workspace_size)
+from . import (PFT, _on_device, ckpt8_scale_shape, mx8_scale_shape, xmoe_add_rmsnorm, xmoe_add_rmsnorm_bwd,
+               xmoe_add_rmsnorm_bwd_workspace_size, xmoe_balance_loss, xmoe_balance_loss_workspace_size, xmoe_build_pft,
+               xmoe_build_pft_shared, xmoe_build_pft_workspace_size, xmoe_combine, xmoe_combine_bwd, xmoe_dispatch,
+               xmoe_dispatch_bwd, xmoe_expert_ffn_bwd, xmoe_expert_ffn_bwd_dact_ckpt8,
+               xmoe_expert_ffn_bwd_dact_ckpt8_workspace_size, xmoe_expert_ffn_bwd_dact_gather, xmoe_expert_ffn_bwd_dw13,
+               xmoe_expert_ffn_bwd_dw13_gather, xmoe_expert_ffn_bwd_dw2, xmoe_expert_ffn_bwd_dx, xmoe_expert_ffn_down,
+               xmoe_expert_ffn_down_mx8, xmoe_expert_ffn_up, xmoe_expert_ffn_up_ckpt8, xmoe_expert_ffn_up_gather,
+               xmoe_expert_ffn_up_mx8, xmoe_layer_few, xmoe_layer_few_mx8, xmoe_layer_few_mx8_workspace_size,
+               xmoe_layer_few_workspace_size, xmoe_mx8_quantize_weights, xmoe_route, xmoe_route_bwd,
+               xmoe_route_bwd_balance, xmoe_route_bwd_workspace_size, xmoe_route_workspace_size)
 
 
 def _on_its_device(method):
@@ -92,6 +94,16 @@ class PaddingFreeMoE:
     them in the backward (the same kernel, so bitwise the same values): what
     the backward needs from the forward shrinks to act, ye and the routing.
 
+    ckpt8=True keeps the pre-activations in 8 bits (whole numbers with a power of
+    two for each 32) and, of the forward's act and ye, nothing: the backward
+    rebuilds act from them and takes the routing weights' gradient from <dA, act>.
+    Gradients are those at the kept values; `dye` then holds dy's rows as they are,
+    act their weights.  The forward's results are the same, bit for bit.
+
+    few=True (forward only: backward=False, at most 64 tokens, no balance loss, shared
+    experts unmerged): the forward is one xmoe_layer_few call, for the next tokens of
+    a few sequences.
+
     Shared experts: a SwiGLU FFN of width n*h is the sum of n FFNs of width h
     over its column blocks.  When the shared width is a multiple of the routed
     h (and merge_shared), the shared experts become that many more experts that
@@ -114,7 +126,11 @@ class PaddingFreeMoE:
 
     def __init__(self, weights: Dict[str, torch.Tensor], T: int, k: int, inv_tau: float = 1.0,
                  backward: bool = True, lean: bool = False, overlap: bool = True, merge_shared: bool = False,
-                 balance_alpha: float = 0.0, n_seq: int = 1):
+                 balance_alpha: float = 0.0, n_seq: int = 1, ckpt8: bool = False, few: bool = False):
+        if ckpt8 and (lean or not backward):
+            raise ValueError("ckpt8 keeps what a backward reads: it needs backward=True, and lean keeps nothing to store")
+        if few and (backward or merge_shared or balance_alpha > 0):
+            raise ValueError("few is forward only (backward=False), without merged shared experts or a balance loss")
         self.w = weights
         wg, w1 = weights["wg"], weights["w1"]
         self.dtype = wg.dtype
@@ -124,7 +140,7 @@ class PaddingFreeMoE:
         self.h = w1.shape[2]
         self.shared = weights.get("s1") is not None
         self.backward_enabled = backward
-        self.lean = lean
+        self.lean, self.ckpt8, self.few = lean, ckpt8, few
         # overlap: the gate's backward and the routed weight gradients run on
         # streams of their own (default priority) beside the data gradients;
         # unmerged shared experts run on a second stream beside the routed path
@@ -134,6 +150,17 @@ class PaddingFreeMoE:
         self.hs = weights["s1"].shape[1] if self.shared else 0
         self.merged = self.shared and merge_shared and self.hs % h == 0
         self.ns = self.hs // h if self.merged else 0       # shared experts carried as routed ones
+        if few:
+            self.side_shared, self.balance_alpha, self.written = False, 0.0, _Written()
+            need = xmoe_layer_few_workspace_size(T, d, E, k, h, self.hs, dt)
+            if need == 0 and T > 0:
+                raise ValueError("few: sizes that xmoe_layer_few does not take (at most 64 tokens)")
+            self.topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+            self.topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+            self.logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+            self.y = torch.empty((T, d), dtype=dt, device=dev)
+            self.few_ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            return
         Ec, kc = E + self.ns, k + self.ns                   # experts and slots per token in the buffer
         self.Ec, self.kc = Ec, kc
         R = T * kc
@@ -167,7 +194,16 @@ class PaddingFreeMoE:
             self.coef = torch.empty((n_seq, E), **f32)
             self.balance_ws = torch.empty(xmoe_balance_loss_workspace_size(T, E, n_seq), dtype=torch.uint8, device=dev)
         self.act = torch.empty((R, h), dtype=dt, device=dev)
-        self.h13 = torch.empty((R, 2 * h), dtype=dt, device=dev) if backward else None
+        self.h13 = torch.empty((R, 2 * h), dtype=dt, device=dev) if backward and not ckpt8 else None
+
+        def kept(rows, width):
+            return (torch.empty((rows, 2 * width), dtype=torch.int8, device=dev),
+                    torch.empty(ckpt8_scale_shape(rows, width), dtype=torch.uint8, device=dev))
+
+        if ckpt8:
+            self.hq, self.hscale = kept(R, h)
+            self.dact_ws = torch.empty(max(xmoe_expert_ffn_bwd_dact_ckpt8_workspace_size(R, h), 16), dtype=torch.uint8,
+                                       device=dev)
         self.ye = torch.empty((R, d), dtype=dt, device=dev)
         self.y = torch.empty((T, d), dtype=dt, device=dev)
         self.side_shared = self.shared and not self.merged
@@ -175,7 +211,9 @@ class PaddingFreeMoE:
             hs = self.hs
             self.sh_off = torch.tensor([0, T], dtype=torch.int32, device=dev)
             self.sh_act = torch.empty((T, hs), dtype=dt, device=dev)
-            self.sh_h13 = torch.empty((T, 2 * hs), dtype=dt, device=dev) if backward else None
+            self.sh_h13 = torch.empty((T, 2 * hs), dtype=dt, device=dev) if backward and not ckpt8 else None
+            if ckpt8:
+                self.sh_hq, self.sh_hscale = kept(T, hs)
             self.sh_y = torch.empty((T, d), dtype=dt, device=dev)
             self.side = torch.cuda.Stream(device=dev)
         if backward:
@@ -255,12 +293,21 @@ class PaddingFreeMoE:
             _need(seq_offsets, (self.n_seq + 1,), (torch.int32,), "seq_offsets", self.device)
             _need(token_mask, (self.T,), (torch.bool, torch.uint8), "token_mask", self.device)
         main, side = self._streams(stream)
+        if self.few:
+            xmoe_layer_few(x, w["wg"], w["w1"], w["w3"], w["w2"], self.k, self.topk_ids, self.topk_w, self.logits, self.y,
+                           self.inv_tau, w.get("logit_bias"), w.get("select_bias"), w.get("s1"), w.get("s3"), w.get("s2"),
+                           workspace=self.few_ws, stream=main)
+            mark("layer_few")
+            return self.y
         keep = self.backward_enabled and not self.lean
         if self.side_shared:
             side.wait_stream(main)
             s1, s3, s2 = self._shared_w()
             around("shared_up", side)
-            xmoe_expert_ffn_up(x, s1, s3, self.sh_off, self.sh_act, h13=self.sh_h13 if keep else None, stream=side)
+            if self.ckpt8:
+                xmoe_expert_ffn_up_ckpt8(x, s1, s3, self.sh_off, self.sh_act, self.sh_hq, self.sh_hscale, stream=side)
+            else:
+                xmoe_expert_ffn_up(x, s1, s3, self.sh_off, self.sh_act, h13=self.sh_h13 if keep else None, stream=side)
             around("shared_up_end", side)
             xmoe_expert_ffn_down(self.sh_act, s2, self.sh_off, self.sh_y, stream=side)
             if side is main:
@@ -284,8 +331,12 @@ class PaddingFreeMoE:
             xmoe_build_pft(self.topk_ids, self.topk_w, self.E, self.pft, self.pft_ws, stream=main)
         mark("build_pft")
         around("up", main)
-        xmoe_expert_ffn_up_gather(x, self.pft.token_ids, self.W1, self.W3, self.pft.expert_offsets, self.act,
-                                  h13=self.h13 if keep else None, stream=main)
+        if self.ckpt8:
+            xmoe_expert_ffn_up_ckpt8(x, self.W1, self.W3, self.pft.expert_offsets, self.act, self.hq, self.hscale,
+                                     token_ids=self.pft.token_ids, stream=main)
+        else:
+            xmoe_expert_ffn_up_gather(x, self.pft.token_ids, self.W1, self.W3, self.pft.expert_offsets, self.act,
+                                      h13=self.h13 if keep else None, stream=main)
         around("up_end", main)
         xmoe_expert_ffn_down(self.act, self.W2, self.pft.expert_offsets, self.ye, stream=main)
         mark("expert_ffn")
@@ -319,8 +370,15 @@ class PaddingFreeMoE:
                 xmoe_expert_ffn_up(self.x, s1, s3, self.sh_off, None, self.sh_h13, stream=side)
                 if side is main:
                     mark("recompute_shared_h13")
-            xmoe_expert_ffn_bwd(self.x, s1, s3, s2, self.sh_act, self.sh_h13, dy, self.sh_off, self.sh_dh13,
-                                self.sh_dx, self._ds1, self._ds3, self._ds2, stream=side)
+            if self.ckpt8:
+                xmoe_expert_ffn_bwd_dact_ckpt8(dy, s2, self.sh_hq, self.sh_hscale, self.sh_off, self.sh_dh13, self.sh_act,
+                                               stream=side)
+                xmoe_expert_ffn_bwd_dx(self.sh_dh13, s1, s3, self.sh_off, self.sh_dx, stream=side)
+                xmoe_expert_ffn_bwd_dw13(self.x, self.sh_dh13, self.sh_off, self._ds1, self._ds3, stream=side)
+                xmoe_expert_ffn_bwd_dw2(self.sh_act, dy, self.sh_off, self._ds2, stream=side)
+            else:
+                xmoe_expert_ffn_bwd(self.x, s1, s3, s2, self.sh_act, self.sh_h13, dy, self.sh_off, self.sh_dh13,
+                                    self.sh_dx, self._ds1, self._ds3, self._ds2, stream=side)
             if side is main:
                 mark("shared_ffn_bwd")
         off = self.pft.expert_offsets
@@ -331,9 +389,23 @@ class PaddingFreeMoE:
         # its dtopk_w the gate's backward
         if ws is not main:
             ws.wait_stream(main)
-        xmoe_combine_bwd(dy, self.ye, self.pft, self.dye, self.dtopk_w_all, stream=ws)
-        if ws is main:
-            mark("combine_bwd")
+        if self.ckpt8:
+            # ye is not kept: dy's rows for dW2 (act carries the weights), and dtopk_w
+            # comes out of dA below, which the gate's backward then waits for
+            xmoe_dispatch(dy, self.kc, self.pft, self.dye, stream=ws)
+            if ws is main:
+                mark("dispatch_dy")
+            xmoe_expert_ffn_bwd_dact_ckpt8(dy, self.W2, self.hq, self.hscale, off, self.dh13, self.act,
+                                           token_ids=self.pft.token_ids, row_weights=self.pft.combine_weights,
+                                           slot_to_row=self.pft.slot_to_row, dweights=self.dtopk_w_all,
+                                           workspace=self.dact_ws, stream=main)
+            mark("bwd_dact")
+            if ws is not main:
+                ws.wait_stream(main)
+        else:
+            xmoe_combine_bwd(dy, self.ye, self.pft, self.dye, self.dtopk_w_all, stream=ws)
+            if ws is main:
+                mark("combine_bwd")
         # the gate's backward needs only the routed slots' dtopk_w, the logits
         # and x: it runs beside the expert backward.  With unmerged shared
         # experts it adds dz . wg^T into their dx; otherwise it writes its own
@@ -358,9 +430,10 @@ class PaddingFreeMoE:
             xmoe_expert_ffn_up_gather(self.x, self.pft.token_ids, self.W1, self.W3, self.pft.expert_offsets,
                                       None, self.h13, stream=main)
             mark("recompute_h13")
-        xmoe_expert_ffn_bwd_dact_gather(dy, self.pft.token_ids, self.pft.combine_weights, self.W2, self.h13, off,
-                                        self.dh13, stream=main)
-        mark("bwd_dact")
+        if not self.ckpt8:
+            xmoe_expert_ffn_bwd_dact_gather(dy, self.pft.token_ids, self.pft.combine_weights, self.W2, self.h13, off,
+                                            self.dh13, stream=main)
+            mark("bwd_dact")
         # weight gradients: dW2 needs act and dye only; dW1/dW3 need dH1/dH3 and
         # the token rows, gathered through the PFT inside their loads
         xmoe_expert_ffn_bwd_dw2(self.act, self.dye, off, self.dW2, stream=ws)
@@ -386,11 +459,18 @@ class PaddingFreeMoE:
 
     def saved_bytes(self) -> int:
         """Bytes the backward needs from the forward (beyond x and the weights):
-        routing results, the PFT, act and ye, plus H1/H3 unless lean."""
+        routing results, the PFT, act and ye, plus H1/H3 unless lean; with ckpt8 the
+        routing, the PFT and H1/H3 in 8 bits.  A layer for few tokens has no backward."""
         def nb(t):
             return 0 if t is None else t.numel() * t.element_size()
-        n = nb(self.topk_ids) + nb(self.topk_w) + nb(self.logits) + nb(self.act) + nb(self.ye)
+        if self.few:
+            return 0
+        n = nb(self.topk_ids) + nb(self.topk_w) + nb(self.logits)
         n += sum(nb(t) for t in self.pft.fields().values())
+        if self.ckpt8:
+            n += nb(self.hq) + nb(self.hscale)
+            return n + (nb(self.sh_hq) + nb(self.sh_hscale) if self.side_shared else 0)
+        n += nb(self.act) + nb(self.ye)
         if not self.lean:
             n += nb(self.h13)
         if self.side_shared:
@@ -484,11 +564,13 @@ class MoEBlock8:
     construction (again by refresh_weights() after they change).  Weights as
     PaddingFreeMoE takes them, with "norm": the gate's and the norm's in bf16,
     the experts' in bf16 or fp32; d, h and the shared width multiples of 32.  Shared experts run on a second stream beside the routed
-    ones.  Holds the buffers of T tokens."""
+    ones.  Holds the buffers of T tokens.  few=True (at most 64 tokens): what follows the
+    norm is one xmoe_layer_few_mx8 call."""
 
     def __init__(self, weights: Dict[str, torch.Tensor], T: int, k: int, inv_tau: float = 1.0, eps: float = 1e-6,
-                 overlap: bool = True):
+                 overlap: bool = True, few: bool = False):
         self.w, self.T, self.k, self.inv_tau, self.eps, self.overlap = weights, T, k, inv_tau, eps, overlap
+        self.few = few
         wg, w1 = weights["wg"], weights["w1"]
         dev, dt = wg.device, wg.dtype
         for n in ("wg", "norm"):
@@ -511,15 +593,23 @@ class MoEBlock8:
         self.topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
         self.topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
         self.logits = torch.empty((T, E), dtype=torch.float32, device=dev)
-        self.pft = PFT(T, E, k, dev)
-        self.pft_ws = torch.empty(max(xmoe_build_pft_workspace_size(T, E, k), 16), **u8)
-        self.route_ws = torch.empty(max(xmoe_route_workspace_size(T, d, E, dt), 16), **u8)
-        self.act, self.acts = rows(R, h)
-        self.ye = torch.empty((R, d), **bf)
         self.w1q, self.w3q, self.w2q = experts(E, h, d), experts(E, h, d), experts(E, d, h)
+        hs = weights["s1"].shape[1] if self.shared else 0
+        self.s1q = self.s3q = self.s2q = None
         if self.shared:
-            hs = weights["s1"].shape[1]
             self.s1q, self.s3q, self.s2q = experts(1, hs, d), experts(1, hs, d), experts(1, d, hs)
+        if few:
+            need = xmoe_layer_few_mx8_workspace_size(T, d, E, k, h, hs)
+            if need == 0 and T > 0:
+                raise ValueError("few: sizes that xmoe_layer_few_mx8 does not take (at most 64 tokens)")
+            self.few_ws = torch.empty(max(need, 16), **u8)
+        else:
+            self.pft = PFT(T, E, k, dev)
+            self.pft_ws = torch.empty(max(xmoe_build_pft_workspace_size(T, E, k), 16), **u8)
+            self.route_ws = torch.empty(max(xmoe_route_workspace_size(T, d, E, dt), 16), **u8)
+            self.act, self.acts = rows(R, h)
+            self.ye = torch.empty((R, d), **bf)
+        if self.shared and not few:
             self.sh_off = torch.tensor([0, T], dtype=torch.int32, device=dev)
             self.sh_act, self.sh_acts = rows(T, hs)
             self.sh_y = torch.empty((T, d), **bf)
@@ -547,9 +637,14 @@ class MoEBlock8:
         """(out, sum)."""
         w = self.w
         main = _on(stream, self.device)
-        side = self.side if self.shared and self.overlap else main
+        side = self.side if self.shared and self.overlap and not self.few else main
         self.written.read(main)
         xmoe_add_rmsnorm(x, residual, w["norm"], self.eps, self.sum, self.y, self.yq, self.yqs, stream=main)
+        if self.few:
+            xmoe_layer_few_mx8(self.y, self.yq, self.yqs, w["wg"], self.w1q, self.w3q, self.w2q, self.k, self.topk_ids,
+                               self.topk_w, self.logits, self.out, self.inv_tau, w.get("logit_bias"), w.get("select_bias"),
+                               self.s1q, self.s3q, self.s2q, workspace=self.few_ws, stream=main)
+            return self.out, self.sum
         if self.shared:
             if side is not main:
                 side.wait_stream(main)
