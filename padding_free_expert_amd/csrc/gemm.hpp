@@ -1347,11 +1347,20 @@ inline hipError_t launch_gemm_dma(const GemmArgs &p, hipStream_t stream) {
 // in ascending k with one fused multiply-add per term, so the fp32 router's
 // logits follow exactly that order.
 
+// A step's values are asked for a step ahead and pass through registers into the other of
+// two shared tiles: one barrier a step, under the products.  An operand's 16 k by 64 rows
+// (or columns) are read in its memory's order, whole 64-byte pieces (2400 rows of 32
+// experts, d = 448, h = 136, up: 147 -> 81 us; the sums and their order are the same).
+// The product behind 8-bit pre-activations keeps sums of 128 k and adds them up (FOLD):
+// its gates' gradients are dot products of whole rows, and one chain of d terms costs
+// them twice the error.
 template <int NB, bool A_KC, bool B_KC, int EPI>
 __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs p) {
     constexpr int BM = 64, BN = 64, BK = 16;
-    __shared__ float As[BK][BM];
-    __shared__ float Bs[NB][BK][BN];
+    // rows of 68: a 16-byte read stays aligned, and a k-major write (16 k by 4 rows or
+    // columns) meets all 64 banks once
+    __shared__ __align__(16) float As[2][BK][BM + 4];
+    __shared__ __align__(16) float Bs[2][NB][BK][BN + 4];
     Tile t;
     if (!resolve_tile<BM, BN>(p, &t, blockIdx.x, gridDim.x)) return;
     const GroupPtrs<float> q = group_ptrs<float>(p, t);
@@ -1364,55 +1373,90 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs p) {
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[b][i][j] = 0.0f;
+    constexpr bool FOLD = EPI == EPI_SWIGLU_BWD_CK8;
+    float sum[FOLD ? NB : 1][4][4] = {};
     const int nph = (p.group_mode == GM_ROWS) ? p.nphase : 1;
-    for (int ph = 0; ph < nph; ++ph) {
+    const int steps = (t.Kg + BK - 1) / BK, total = steps * nph;
+    // element i of this thread: (k, row) of A, (k, column) of B
+    auto ak = [&](int i) { const int e = threadIdx.x + 256 * i; return A_KC ? e % BK : e / BM; };
+    auto am = [&](int i) { const int e = threadIdx.x + 256 * i; return A_KC ? e / BK : e % BM; };
+    auto bk = [&](int i) { const int e = threadIdx.x + 256 * i; return B_KC ? e % BK : e / BN; };
+    auto bn = [&](int i) { const int e = threadIdx.x + 256 * i; return B_KC ? e / BK : e % BN; };
+    float ra[4], rb[NB][4];
+    auto fetch = [&](int step) {
+        const int ph = step / steps, k0 = (step - ph * steps) * BK;
         const float *A = ph ? q.A1 : q.A0;
         const float *B0 = ph ? q.B1 : q.B0;
-        for (int k0 = 0; k0 < t.Kg; k0 += BK) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int e = threadIdx.x + 256 * i;  // 0..1023 over the 16x64 tile
-                const int kk = e / BM, mm = e % BM;
-                const int gm = m0 + mm, gk = k0 + kk;
-                float va = 0.0f;
-                if (gm < t.Mg && gk < t.Kg) {
-                    if (A_KC && p.a_map && p.group_mode == GM_ROWS)
-                        va = static_cast<const float *>(p.A0)[static_cast<int64_t>(p.a_map[t.base + gm]) * p.lda + gk];
-                    else if (!A_KC && p.a_map && p.group_mode == GM_KSPLIT)
-                        va = static_cast<const float *>(p.A0)[static_cast<int64_t>(p.a_map[t.base + gk]) * p.lda + gm];
-                    else
-                        va = A_KC ? A[static_cast<int64_t>(gm) * p.lda + gk] : A[static_cast<int64_t>(gk) * p.lda + gm];
-                }
-                As[kk][mm] = va;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const int gn = n0 + mm;
-                    float vb = 0.0f;
-                    const float *Bm = b ? q.Bx : B0;
-                    if (gn < p.N && gk < t.Kg)
-                        vb = B_KC ? Bm[static_cast<int64_t>(gn) * p.ldb + gk] : Bm[static_cast<int64_t>(gk) * p.ldb + gn];
-                    Bs[b][kk][mm] = vb;
-                }
+        for (int i = 0; i < 4; ++i) {
+            const int gm = m0 + am(i), gk = k0 + ak(i);
+            float va = 0.0f;
+            if (gm < t.Mg && gk < t.Kg) {
+                if (A_KC && p.a_map && p.group_mode == GM_ROWS)
+                    va = static_cast<const float *>(p.A0)[static_cast<int64_t>(p.a_map[t.base + gm]) * p.lda + gk];
+                else if (!A_KC && p.a_map && p.group_mode == GM_KSPLIT)
+                    va = static_cast<const float *>(p.A0)[static_cast<int64_t>(p.a_map[t.base + gk]) * p.lda + gm];
+                else
+                    va = A_KC ? A[static_cast<int64_t>(gm) * p.lda + gk] : A[static_cast<int64_t>(gk) * p.lda + gm];
             }
-            __syncthreads();
+            ra[i] = va;
+            const int gn = n0 + bn(i), gkb = k0 + bk(i);
 #pragma unroll
-            for (int kk = 0; kk < BK; ++kk) {
-                float a[4], bv[NB][4];
+            for (int b = 0; b < NB; ++b) {
+                float vb = 0.0f;
+                const float *Bm = b ? q.Bx : B0;
+                if (gn < p.N && gkb < t.Kg)
+                    vb = B_KC ? Bm[static_cast<int64_t>(gn) * p.ldb + gkb] : Bm[static_cast<int64_t>(gkb) * p.ldb + gn];
+                rb[b][i] = vb;
+            }
+        }
+    };
+    if (total > 0) fetch(0);
+    for (int step = 0; step < total; ++step) {
+        const int s = step & 1;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = As[kk][ty * 4 + i];
+        for (int i = 0; i < 4; ++i) {
+            As[s][ak(i)][am(i)] = ra[i];
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+            for (int b = 0; b < NB; ++b) Bs[s][b][bk(i)][bn(i)] = rb[b][i];
+        }
+        __syncthreads();  // the tile is whole; the other one's readers are past the barrier before
+        if (step + 1 < total) fetch(step + 1);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) bv[b][j] = Bs[b][kk][tx * 4 + j];
+        for (int kk = 0; kk < BK; ++kk) {
+            typedef float f4_t __attribute__((ext_vector_type(4)));
+            const f4_t a = *reinterpret_cast<const f4_t *>(&As[s][kk][ty * 4]);
+            f4_t bv[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) bv[b] = *reinterpret_cast<const f4_t *>(&Bs[s][b][kk][tx * 4]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[b][i][j] = __builtin_fmaf(a[i], bv[b][j], acc[b][i][j]);
+        }
+        if constexpr (FOLD) {
+            if (step % 8 == 7) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[b][i][j] = __builtin_fmaf(a[i], bv[b][j], acc[b][i][j]);
+                        for (int j = 0; j < 4; ++j) {
+                            sum[b][i][j] += acc[b][i][j];
+                            acc[b][i][j] = 0.0f;
+                        }
             }
-            __syncthreads();
         }
+    }
+    if constexpr (FOLD) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[b][i][j] += sum[b][i][j];
     }
     if constexpr (EPI == EPI_SWIGLU_CK8 || EPI == EPI_SWIGLU_BWD_CK8) {
         // a thread's four columns lie in one block of 32, the eight threads tx ^ 0..7 hold it
