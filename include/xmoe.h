@@ -647,8 +647,9 @@ xmoe_status xmoe_expert_ffn_down_mx8(const void *act, const void *act_scale, con
  *   logits, topk_ids, topk_w : as xmoe_route
  *   a[t,j] = silu(x[t] . w1[e]) * (x[t] . w3[e]),  e = topk_ids[t,j]
  *   y[t]   = sum_j topk_w[t,j] * (a[t,j] . w2[e])  (+ the shared experts' FFN of x[t])
- * fp32 sums; a is rounded once to the dtype, y once at the end (the experts'
- * outputs are not rounded in between, as xmoe_expert_ffn_down does).  The sums run
+ * fp32 sums; y is rounded once, at the end: a is not rounded to the dtype on the way
+ * (bf16: held as the sum of two bf16 values, within 2^-16 of it), nor the experts'
+ * outputs, as xmoe_expert_ffn_up and _down do.  The sums run
  * in another order than xmoe_route's and xmoe_expert_ffn_up's, so that results
  * agree to rounding, and experts whose selection values differ by less than that
  * may be chosen the other way round.  Whatever the logits hold, a token's ids are
@@ -673,7 +674,9 @@ xmoe_status xmoe_layer_few(const void *x, const void *wg, const void *w1, const 
 /*
  * The same on 8-bit rows and weights (bf16 gate, x and y): the gate reads x, the
  * experts xq with xscale (8-bit rows [T,d]), and a is held in 8 bits, quantized from
- * fp32, as xmoe_expert_ffn_up_mx8 leaves it; products and their error as there.
+ * fp32, as xmoe_expert_ffn_up_mx8 leaves it.  Weights, rows and a are opened to bf16,
+ * which holds their values (those below 2^-126 in magnitude count as zeros), and
+ * multiplied with ordinary fp32 sums, not with the scaled instruction's cuts.
  * Weights as xmoe_mx8_quantize_weights lays them out; the shared experts as one
  * expert of width hs.  d, h, hs multiples of 32; other limits as xmoe_layer_few, with
  * one byte an element for the experts' matrices.  The structs are read during the call.

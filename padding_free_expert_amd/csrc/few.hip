@@ -119,7 +119,14 @@ struct FewArgs {
 template <typename T>
 struct PlainCore {
     using Elt = T;
-    using Act = T;
+    // An activation is held in 32 bits: fp32, or for bf16's products as the sum of two
+    // bf16 values, 2^-17 from it (rounded to one it adds an error of y's own rounding's
+    // size, 1.4 times as much in all; the second product waits for no memory: level).
+    // Eight of them are eight first halves, then eight second ones.
+    struct Pair {
+        bf16_t v[2];
+    };
+    using Act = std::conditional_t<sizeof(T) == 2, Pair, float>;
     static constexpr bool kMx = false;
     static constexpr int CV = 16 / static_cast<int>(sizeof(T)), BN = 16 * CV, STEP = 32;
     static constexpr int kStage = 16;  // no staging
@@ -128,6 +135,9 @@ struct PlainCore {
     static constexpr int kPart = 1024 / static_cast<int>(sizeof(T));
     struct X {
         i32x4_t v[sizeof(T) / 2];  // eight elements of a row
+    };
+    struct XAct {
+        i32x4_t v[2];              // eight activations
     };
     // of x [rows, d]: the eight elements at k + 8 (l / 16)
     struct Raw {
@@ -142,11 +152,12 @@ struct PlainCore {
     }
     __device__ static __forceinline__ void open_row(const Raw &r, X &x) { x = r.x; }
     // of a row of activations in shared memory, k from the part's start
-    __device__ static __forceinline__ void act_row(const char *row, int k, int lane, X &x) {
+    __device__ static __forceinline__ void act_row(const char *row, int k, int lane, XAct &x) {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(X) / 16); ++i)
-            x.v[i] = reinterpret_cast<const i32x4_t *>(row + (k + 8 * (lane >> 4)) * static_cast<int>(sizeof(T)))[i];
+        for (int i = 0; i < 2; ++i) x.v[i] = reinterpret_cast<const i32x4_t *>(row + (k + 8 * (lane >> 4)) * 4)[i];
     }
+    // bytes from a row's start to the activations c, c + 1, ...
+    __device__ static __forceinline__ int act_at(int c) { return sizeof(T) == 2 ? 32 * (c >> 3) + 2 * (c & 7) : 4 * c; }
 
     template <int M, int WK, class Rows>
     struct Product {
@@ -183,7 +194,7 @@ struct PlainCore {
             fetch(k, p, rows);
         }
         __device__ __forceinline__ void multiply(const Step &s, int at_k, const Rows &rows) {
-            X x[M];
+            typename Rows::X x[M];
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 if constexpr (Rows::kEarly) open_row(s.x[m], x[m]);
@@ -200,9 +211,11 @@ struct PlainCore {
                                                                       static_cast<uint32_t>(s.w[2 * z][i / 2]),
                                                                       i % 2 ? 0x07060302u : 0x05040100u));
 #pragma unroll
-                    for (int m = 0; m < M; ++m)
-                        acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8_t, o), __builtin_bit_cast(bf16x8_t, x[m].v[0]), acc[m][i], 0, 0, 0);
+                    for (int h = 0; h < static_cast<int>(sizeof(x[0].v) / 16); ++h)
+#pragma unroll
+                        for (int m = 0; m < M; ++m)
+                            acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(bf16x8_t, o), __builtin_bit_cast(bf16x8_t, x[m].v[h]), acc[m][i], 0, 0, 0);
                 }
             } else {
 #pragma unroll
@@ -275,6 +288,7 @@ struct Mx8Core {
     struct X {
         i32x4_t v[4];   // elements 32 (l / 16) + 8 z of the row's 128
     };
+    using XAct = X;
     struct Raw {
         i32x4_t v[2];
         int s;
@@ -301,6 +315,7 @@ struct Mx8Core {
 #pragma unroll
         for (int z = 0; z < 4; ++z) x.v[z] = *reinterpret_cast<const i32x4_t *>(row + 2 * (k + 32 * (lane >> 4) + 8 * z));
     }
+    __device__ static __forceinline__ int act_at(int c) { return 2 * c; }
 
     template <int M, int WK, class Rows>
     struct Product {
@@ -421,8 +436,8 @@ __device__ __forceinline__ int fresh(int v) {
 
 // The waves' parts of 16 rows x BN columns, those of each WK waves added in wave order:
 // thread tid has row tid / 16, columns CV (tid % 16) ..
-template <class C, int WK>
-__device__ __forceinline__ void sum_waves(FewShared<C> &sh, const f32x4_t (&acc)[C::CV], int lane, int wave,
+template <class C, int WK, class Shared>
+__device__ __forceinline__ void sum_waves(Shared &sh, const f32x4_t (&acc)[C::CV], int lane, int wave,
                                           float (&out)[kFewWaves / WK][C::CV]) {
     __syncthreads();
     C::each(acc, fresh(lane), [&](int c, f32x4_t v) { *reinterpret_cast<f32x4_t *>(&sh.red[wave][lane & 15][c]) = v; });
@@ -473,6 +488,7 @@ __device__ __forceinline__ const uint8_t *scales_at(const uint8_t *s, int64_t e,
 // The rows of x as operands, asked for with the weights; slot nullptr: row r is token r.
 template <class C, int M>
 struct RowsOfX {
+    using X = typename C::X;
     static constexpr bool kEarly = true;
     const FewArgs &p;
     int t[M], lane;
@@ -720,12 +736,22 @@ struct ActTile {
     static constexpr int LD = KP * static_cast<int>(sizeof(typename C::Act)) + 16;  // 16 more: neighbouring rows on other banks
     __align__(16) char v[16 * MT][LD];
 };
+// What a block of the down-projection keeps there; its waves' sums take the activations'
+// place, which are read by then.
+template <class C, int MT, int KP, int WK>
+struct DownShared : FewStage<C> {
+    union {
+        ActTile<C, MT, KP> act;
+        float red[WK == 1 ? 1 : kFewWaves][16][C::BN + 4];
+    };
+};
 template <class C, int MT, int KP>
 struct RowsOfAct {
+    using X = typename C::XAct;
     static constexpr bool kEarly = false;
     const ActTile<C, MT, KP> &t;
     int ka, lane;
-    __device__ __forceinline__ void read(int m, int k, typename C::X &x) const {
+    __device__ __forceinline__ void read(int m, int k, X &x) const {
         C::act_row(t.v[16 * m + (lane & 15)], k - ka, lane, x);
     }
 };
@@ -754,8 +780,18 @@ __device__ __forceinline__ void form_act(const FewFfn &f, int sl, int c, bool in
         i32x4_t u[2];
         open8(i32x4_t{static_cast<int>(o[0]), 0, 0, 0}, static_cast<int>(byte), u);
         *reinterpret_cast<uint2 *>(out) = make_uint2(static_cast<uint32_t>(u[0][0]), static_cast<uint32_t>(u[0][1]));
-    } else if constexpr (sizeof(typename C::Act) == 2) {
-        *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    } else if constexpr (sizeof(typename C::Elt) == 2) {
+        const uint2 hi = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        const float of[4] = {__uint_as_float(hi.x << 16), __uint_as_float(hi.x & 0xffff0000u), __uint_as_float(hi.y << 16),
+                             __uint_as_float(hi.y & 0xffff0000u)};
+        float lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = v[i] - of[i];
+            if (!(fabsf(lo[i]) < INFINITY)) lo[i] = 0.0f;  // behind an infinity or a NaN
+        }
+        *reinterpret_cast<uint2 *>(out) = hi;
+        *reinterpret_cast<uint2 *>(out + 16) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
     } else {
         *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
     }
@@ -767,7 +803,7 @@ __device__ __forceinline__ void act_wave(const FewFfn &f, int b) {
     const int per = (f.h + 255) / 256, sl = b / per, c = 256 * (b % per) + 4 * static_cast<int>(threadIdx.x);
     // whole blocks of 32 columns (8 bits) are in or out
     if (c < f.h)
-        form_act<C>(f, sl, c, true, static_cast<char *>(f.act) + sizeof(typename C::Act) * (static_cast<int64_t>(sl) * f.h + c));
+        form_act<C>(f, sl, c, true, static_cast<char *>(f.act) + sizeof(typename C::Act) * static_cast<int64_t>(sl) * f.h + C::act_at(c));
 }
 
 // between 3 and 4, where few experts with many rows each are cut into many parts
@@ -794,8 +830,8 @@ __global__ __launch_bounds__(64) void few_topk_kernel(FewArgs p) {
 // waits being gone)
 template <class C, int MT, int KP, int WK>
 __global__ __launch_bounds__(kFewThreads, few_occ(MT)) void few_down_kernel(FewArgs p, int units) {
-    __shared__ std::conditional_t<WK == 1, FewStage<C>, FewShared<C>> sh;
-    __shared__ ActTile<C, MT, KP> act;
+    __shared__ DownShared<C, MT, KP, WK> sh;
+    ActTile<C, MT, KP> &act = sh.act;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int b = static_cast<int>(blockIdx.x);
     const bool shared = b >= units;
@@ -825,7 +861,7 @@ __global__ __launch_bounds__(kFewThreads, few_occ(MT)) void few_down_kernel(FewA
         constexpr int kNext = kFewWaves / WK * C::BN;  // from a wave's strip to its next
         const int first = n0 + (WK == 1 ? wave * C::BN : 0);
         if (first < n1) pr.start(first, rows);
-        __syncthreads();  // the rows before have been read
+        __syncthreads();  // the rows before have been read, and their sums
         using Act = typename C::Act;
         if (f.act) {
             constexpr int V = 16 / static_cast<int>(sizeof(Act));
@@ -838,7 +874,7 @@ __global__ __launch_bounds__(kFewThreads, few_occ(MT)) void few_down_kernel(FewA
         } else {
             for (int i = threadIdx.x; i < nr * (len / 4); i += kFewThreads) {
                 const int r = i / (len / 4), c = 4 * (i % (len / 4));
-                form_act<C>(f, slot ? slot[r0 + r] : r0 + r, ka + c, ka + c < kb, act.v[r] + sizeof(Act) * c);
+                form_act<C>(f, slot ? slot[r0 + r] : r0 + r, ka + c, ka + c < kb, act.v[r] + C::act_at(c));
             }
         }
         __syncthreads();

@@ -1,10 +1,12 @@
 """64-bit definition of the whole layer for a few tokens, with the error that the
 formats allow to each result.
 
-Roundings: an activation is rounded once (bf16: half a step, 2^-8 of it; fp32 2^-24;
-8 bits: 2^-4 of it, or half of the smallest step, 2^-10, times the block's scale), y
-once more.  A sum of K products in fp32 is off by at most K 2^-24 of the sum of their
-magnitudes; the scaled matrix instruction's by 2^-10 more.  silu(a) moves by at most
+Roundings: an activation is held in fp32 (2^-24 of it), for bf16 as the sum of two bf16
+values (half a step of the second, which is at most half a step of the first: 2^-16 of it
+at most), with 8 bits rounded to them (2^-4 of it, or half of the smallest step, 2^-10,
+times the block's scale); y is rounded once.  A sum of K products in fp32 is off by at
+most K 2^-24 of the sum of their magnitudes (the down-projection of bf16 has 2 h products,
+two for an activation).  silu(a) moves by at most
 1.1 times a's own error, exp and the division by 2^-20 of the value."""
 from __future__ import annotations
 
@@ -19,13 +21,13 @@ def silu(a):
     return a * torch.sigmoid(a)
 
 
-def ffn(x, w1, w3, w2, act_half, sum_err):
+def ffn(x, w1, w3, w2, act_half):
     """(values, allowed error) of one SwiGLU FFN on float64 rows; act_half None: act in
-    8 bits, else half a step of its rounding."""
+    8 bits, else the part of it that is lost."""
     K, h = w1.shape[0], w1.shape[1]
     a, b = x @ w1, x @ w3
-    d1 = (K * 2.0 ** -24 + sum_err) * (x.abs() @ w1.abs())
-    d3 = (K * 2.0 ** -24 + sum_err) * (x.abs() @ w3.abs())
+    d1 = K * 2.0 ** -24 * (x.abs() @ w1.abs())
+    d3 = K * 2.0 ** -24 * (x.abs() @ w3.abs())
     v = silu(a) * b
     dv = 1.1 * d1 * (b.abs() + d3) + silu(a).abs() * d3 + 2.0 ** -20 * v.abs()
     if act_half is None:
@@ -38,7 +40,7 @@ def ffn(x, w1, w3, w2, act_half, sum_err):
     else:
         act = v
         da = act_half * (v.abs() + dv) + dv
-    return act @ w2, da @ w2.abs() + (h * 2.0 ** -24 + sum_err) * ((act.abs() + da) @ w2.abs())
+    return act @ w2, da @ w2.abs() + 2 * h * 2.0 ** -24 * ((act.abs() + da) @ w2.abs())
 
 
 def gate(x, wg, tau, lbias):
@@ -51,7 +53,7 @@ def gate(x, wg, tau, lbias):
     return z, dz
 
 
-def layer(x, xe, wg, sets, shared, ids, tau=1.0, lbias=None, act_half=None, sum_err=0.0, out_half=0.0):
+def layer(x, xe, wg, sets, shared, ids, tau=1.0, lbias=None, act_half=None, out_half=0.0):
     """y and its allowed error for the given ids.  x: the gate's rows, xe: the experts';
     sets(e) and shared: (w1, w3, w2) in float64."""
     z, dz = gate(x, wg, tau, lbias)
@@ -60,12 +62,12 @@ def layer(x, xe, wg, sets, shared, ids, tau=1.0, lbias=None, act_half=None, sum_
     y, dy = torch.zeros_like(xe), torch.zeros_like(xe)
     for e in torch.unique(ids).tolist():
         t = torch.nonzero((ids == e).any(1)).flatten()
-        v, dv = ffn(xe[t], *sets(e), act_half, sum_err)
+        v, dv = ffn(xe[t], *sets(e), act_half)
         w, dw = p[t, e, None], dp[t, e, None]
         y[t] += w * v
         dy[t] += w * dv + dw * (v.abs() + dv)
     if shared is not None:
-        v, dv = ffn(xe, *shared, act_half, sum_err)
+        v, dv = ffn(xe, *shared, act_half)
         y += v
         dy += dv
     return z, dz, p, dp, y, dy + (out_half + 2.0 ** -20) * (y.abs() + dy)

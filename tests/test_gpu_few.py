@@ -76,11 +76,11 @@ class Case:
         if self.mx8:
             of = lambda w, e: tuple(ref.mx8_weights(q[e], s[e]) for q, s in w)
             xe = ref.mx8_values(self.xq, self.xs)
-            how = dict(act_half=None, sum_err=2.0 ** -10)
+            act_half = None
         else:
             of = lambda w, e: tuple(t[e].to(D) for t in w)
             xe = self.x.to(D)
-            how = dict(act_half=ref.half_step(self.dt), sum_err=0.0)
+            act_half = 2.0 ** -16 if self.dt == torch.bfloat16 else 2.0 ** -24
         shared = None
         if self.hs:
             shared = of(self.s, 0) if self.mx8 else tuple(t.to(D) for t in self.s)
@@ -88,7 +88,7 @@ class Case:
         assert int(ids.min()) >= 0 and int(ids.max()) < self.E, name
         assert all(len(set(r)) == self.k for r in ids.tolist()), name
         z, dz, p, dp, y, dy = ref.layer(self.x.to(D), xe, self.wg.to(D), lambda e: of(self.w, e), shared, ids, tau=self.tau,
-                                        lbias=self.lb, out_half=ref.half_step(self.dt), **how)
+                                        lbias=self.lb, out_half=ref.half_step(self.dt), act_half=act_half)
         assert ref.chosen_well(z, dz, self.sb, self.ids), name
         for what, got, want, tol in (("logits", self.z, z, dz + 2.0 ** -24 * z.abs()),
                                      ("topk_w", self.p, torch.gather(p, 1, ids), torch.gather(dp, 1, ids)),
