@@ -223,7 +223,9 @@ hipError_t launch_ffn_up_ckpt8(int dt, const void *xs, const int32_t *row_map, i
 
 namespace {
 
-// dweights of slot i (row slot_to_row[i], or i): the column tiles' parts in order.
+// dweights of slot i (row slot_to_row[i], or i): the parts of 128 columns (fp32: 64) in
+// order.  4 us for 24576 rows of 11 parts, a launch's start for the most part; sums by
+// atomics in the product's kernel would change with the order of its blocks.
 // Rows in no segment keep what they hold.
 __global__ __launch_bounds__(256) void ckpt8_dots_kernel(const float *__restrict__ part, int tiles, int64_t rows,
                                                          const int32_t *__restrict__ offsets, int E,
@@ -238,7 +240,9 @@ __global__ __launch_bounds__(256) void ckpt8_dots_kernel(const float *__restrict
     out[i] = v;
 }
 
-// hq, hscale -> [H1 | H3]: a thread for eight columns of a row
+// hq, hscale -> [H1 | H3], q 2^(b - 127): a thread for eight columns of a row, whose bytes
+// and values lie side by side over a wave.  Bound by its bytes: 24576 rows of h = 1408 in
+// bf16 (208 MB) 40 us, 5.2 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void ckpt8_dequantize_kernel(const uint8_t *__restrict__ hq,
                                                                const uint8_t *__restrict__ hs, int64_t rows, int h,
@@ -273,6 +277,11 @@ hipError_t launch_ckpt8_dequantize(int dt, const void *hq, const void *hscale, i
     return hipGetLastError();
 }
 
+// Results larger than the last-level cache pass it by: 262144 rows of h = 1024 (1.6 GB)
+// 2565 -> 2497 us; 24576 rows of 1408 (208 MB), which the next products find there, 250 ->
+// 251 the other way.
+constexpr double kCacheBytes = 256.0 * 1024 * 1024;
+
 // launch_ffn_bwd_dact with H1 and H3 in 8 bits; also act (times the row's scale) and, in
 // dweights, <dA, act> of each row before that scale.  ws: [column tiles, rows] floats
 // (64 columns a tile at least).
@@ -300,8 +309,9 @@ hipError_t launch_ffn_bwd_dact_ckpt8(int dt, const void *dye, const int32_t *row
     p.ck_scale = static_cast<uint8_t *>(const_cast<void *>(hscale));
     p.ck_act = act;
     p.ck_dots = dweights ? static_cast<float *>(ws) : nullptr;
+    p.ck_stream = static_cast<double>(rows) * h * 6.0 > kCacheBytes;
     // tiles by launch_ffn_bwd_dact's rule
-    const int bn = dt == kBF16 ? 256 : 64;
+    const int bn = dt == kBF16 ? 128 : 64;  // columns of a part of a row's sum
     hipError_t err = dt != kBF16 ? launch_gemm_f32<1, true, true, EPI_SWIGLU_BWD_CK8>(p, s)
                      : large_tiles_filled(rows, E, h, 256)
                          ? launch_gemm_dma<256, 256, 32, 4, 2, 1, true, true, 4, EPI_SWIGLU_BWD_CK8, bf16_t, 1>(p, s)

@@ -60,6 +60,7 @@ struct GemmArgs {
     // [2, ceil(N / 128), extent, 4]
     uint8_t *ck_scale;
     void *ck_act;            // EPI_SWIGLU_BWD_CK8: row_scale * silu(H1) * H3 [extent, N]
+    bool ck_stream;          // ... results pass the caches by
     float *ck_dots;          // ... [column tiles, extent] parts of <dA, silu(H1) * H3> (optional)
     float scale;             // EPI_ROUTER
     const float *col_bias;   // EPI_ROUTER (optional)
@@ -472,6 +473,13 @@ __device__ __forceinline__ void wait_vmem() {
     asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
 
+// A wave's accesses to shared memory are served in order: this keeps the compiler from
+// moving those of one lane past those of another.
+__device__ __forceinline__ void wave_order() {
+    asm volatile("" : : : "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
 __device__ __forceinline__ bf16x8_t lds_read_frag16(uint32_t a) {
     return *reinterpret_cast<const lds_bf16x8_t *>(static_cast<uintptr_t>(a));
 }
@@ -588,13 +596,57 @@ struct FragAddr {
     }
 };
 
+// What a wave of EPI_SWIGLU_BWD_CK8 asks for before its products: the bytes of its first 32
+// rows (as the epilogue's shared memory holds them), its rows' scales and weights.
+struct NoBytes {
+    __device__ __forceinline__ void load(const GemmArgs &, const Tile &, const GroupPtrs<bf16_t> &, int, int, int) {}
+};
+struct BackBytes {
+    typedef int i32x4_t __attribute__((ext_vector_type(4)));
+    __amdgpu_buffer_rsrc_t rs;
+    i32x4_t h[2][4];
+    uint32_t sc[2][2];  // dword of a row and 128 columns
+    float w[2];
+    // byte of the 16 that lane `lane` takes of KiB x of 32 rows x 128 columns
+    __device__ __forceinline__ static int at(const GemmArgs &p, int i, int x, int wcol, int lane) {
+        const int row = i * 32 + 8 * x + lane / 8, col = wcol + 16 * ((lane & 7) ^ (row & 7));
+        return col < p.N ? static_cast<int>(row * p.ld_aux + col) : kOob;
+    }
+    __device__ __forceinline__ void load(const GemmArgs &p, const Tile &t, const GroupPtrs<bf16_t> &q, int wrow, int wcol,
+                                         int lane) {
+        const int groups = (p.N + 127) / 128;
+        rs = make_rsrc(static_cast<const uint8_t *>(p.aux) + (q.crow + wrow) * p.ld_aux,
+                       static_cast<int64_t>(max(t.Mg - wrow, 0)) * p.ld_aux);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int off = at(p, 0, x, wcol, lane);
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                h[b][x] = __builtin_bit_cast(
+                    i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, off == kOob ? kOob : off + b * p.hoff, 0, 0));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int m = wrow + i * 32 + (lane & 31);
+            const bool live = m < t.Mg && wcol < p.N;
+            w[i] = p.row_scale && live ? p.row_scale[q.crow + m] : 1.0f;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                sc[b][i] = live ? *reinterpret_cast<const uint32_t *>(
+                                      p.ck_scale + ((static_cast<int64_t>(b) * groups + wcol / 128) * p.extent + q.crow + m) * 4)
+                                : 0x7f7f7f7fu;
+        }
+    }
+};
+
 // The epilogue of a BM x BN tile held as accumulators acc[NB][TM][TN] by
 // WGM x WGN waves (the layout both pipelined kernels produce), with the
 // kernel's idle operand ring (RING bytes of LDS at smem / sbase) as staging.
-template <int BM, int BN, int WGM, int WGN, int NB, int RING, int EPI, typename OutT>
+template <int BM, int BN, int WGM, int WGN, int NB, int RING, int EPI, typename OutT, typename Bytes>
 __device__ __forceinline__ void gemm_epilogue(const GemmArgs &p, const Tile &t, const GroupPtrs<bf16_t> &q,
                                               f32x16_t (&acc)[NB][BM / WGM / 32][BN / WGN / 32], char *smem,
-                                              uint32_t sbase, int m0, int n0, int lane, int wave) {
+                                              uint32_t sbase, int m0, int n0, int lane, int wave,
+                                              const Bytes &bytes) {
     constexpr int NW = WGM * WGN, NT = 64 * NW;
     constexpr int WTM = BM / WGM, WTN = BN / WGN;
     constexpr int TM = WTM / 32, TN = WTN / 32;
@@ -669,7 +721,11 @@ __device__ __forceinline__ void gemm_epilogue(const GemmArgs &p, const Tile &t, 
         return;
     }
     if constexpr (EPI == EPI_SWIGLU_CK8) {
-        // act as above; H1 and H3 in 8 bits.  A lane holds 16 of the 32 columns of
+        // act as above; H1 and H3 in 8 bits: per 32 columns the byte b whose 2^(b - 127)
+        // brings the largest magnitude to at most 127, values rounded to whole steps.
+        // Bound by the products (24576 rows of 64 experts, d = 2048, h = 1408: 368 us, of
+        // d = 4096, 160 experts, h = 1024 991 TFLOP/s; without H1 and H3 352 and 1033, with
+        // them in bf16 372 and 997).  A lane holds 16 of the 32 columns of
         // product (i, j) for its row, lane ^ 32 the others: a scale block is one
         // product's row, and its columns past N are zeros, which change nothing.
         constexpr int LDC = BN + 8, LDQ = BN + 8;
@@ -753,154 +809,132 @@ __device__ __forceinline__ void gemm_epilogue(const GemmArgs &p, const Tile &t, 
         return;
     }
     if constexpr (EPI == EPI_SWIGLU_BWD_CK8) {
-        // H1 and H3 come as bytes by LDS DMA (both tiles of the block at once: they
-        // fit the ring), each lane takes those of its accumulators' places into
-        // registers and turns dA in place into dH1, dH3 and act, which leave through
-        // the ring as in the store epilogue.  16-byte chunk c of tile row r sits at
-        // chunk c ^ (r % 16).
-        constexpr int kCpr = BN / 16;  // chunks a row
-        static_assert(NB == 1 && kCpr == 16, "256 columns");
-        static_assert(2 * BM * BN <= RING, "both tiles of bytes must fit the ring");
-        constexpr int kBlk = BM * BN / 1024;  // 1 KiB loads per tile
-        static_assert(kBlk % NW == 0, "whole loads per wave");
-        constexpr int LDC = BN + 8;
-        constexpr int kPass = BM * LDC * 2 <= RING ? 1 : WGM;
-        constexpr int RP = BM / kPass;
-        static_assert(RP * LDC * 2 <= RING && WGN * BM * 4 <= RING, "output tile must fit the ring");
+        // Each wave by itself, in its own piece of the ring (no barrier between waves:
+        // one's stores are under way while another computes).  H1 and H3 of its rows come
+        // as bytes by LDS DMA, 32 rows of them (a product's) at a time turn dA in place
+        // into dH1, dH3 and act, and these leave in 16-byte chunks through the bytes'
+        // place.  16-byte chunk c of row r sits at chunk c ^ (r % 8) (bytes), c ^ (r % 16)
+        // (values).
+        // The first 32 rows' bytes were asked for before the products; the others' come
+        // while these are worked on.
+        //   s = 1 / (1 + e^-H1):  dH1 = w dA H3 s (1 + H1 (1 - s)),  dH3 = w dA H1 s,
+        //   act = w H1 s H3,  part of dw = <dA, H1 s H3>   (w: the row's weight or 1)
+        // Bound: the products, then 8 bytes a value here (2 read, 6 written), which one
+        // 256-row tile on a compute unit has nothing to hide behind.  24576 rows of 64
+        // experts, d = 2048, h = 1408: 245 us, 175 without this epilogue (1180 TFLOP/s for
+        // whole tiles), 57 being its bytes at a copy's 4.9 TB/s; 262144 rows of 160, d =
+        // 4096, h = 1024: 2495 us, 881 TFLOP/s (by blocks, a barrier between steps: 2612).
+        // 128-row tiles, two on a compute unit, overlap but multiply slower: 265 and 2725.
+        static_assert(NB == 1 && WTN == 128 && TM == 2, "a wave's row is one dword of scales");
+        static_assert(WGM * WGN * 2 * WTM * WTN <= RING, "both tiles of bytes must fit the ring");
         typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
         typedef float f2_t __attribute__((ext_vector_type(2)));
-        const int groups = (p.N + 127) / 128;
-        const __amdgpu_buffer_rsrc_t raux = make_rsrc(static_cast<const uint8_t *>(p.aux) + (q.crow + m0) * p.ld_aux,
-                                                      static_cast<int64_t>(t.Mg - m0) * p.ld_aux);
+        typedef typename Bytes::i32x4_t i32x4_t;
+        const int wrow = m0 + wm * WTM, wcol = n0 + wn * WTN;  // the wave's first row and column
         __syncthreads();  // every wave is done with the ring
+        if (wrow >= t.Mg || wcol >= p.N) return;
+        char *const mine = smem + wave * (2 * WTM * WTN);
+        const uint32_t smine = sbase + wave * (2 * WTM * WTN);
 #pragma unroll
-        for (int x = 0; x < kBlk / NW; ++x) {
-            const int blk = x * NW + wave;
-            const int o = blk * 1024 + lane * 16;
-            const int row = o / BN, c = ((o % BN) / 16) ^ (row & 15);
-            const int col = n0 + 16 * c;
-            const int off = static_cast<int>(row * p.ld_aux + col);
-            lds_dma16(raux, col < p.N ? off : kOob, sbase + blk * 1024);
-            lds_dma16(raux, col < p.N ? off + p.hoff : kOob, sbase + BM * BN + blk * 1024);
-        }
-        // scales of the lane's rows: dword (row, 128 columns) and the row's weight
-        float rsc[TM], dot[TM];
-        uint32_t sc[2][TM][WTN / 128];
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int m = m_lane + i * 32;
-            rsc[i] = p.row_scale && m < t.Mg ? p.row_scale[q.crow + m] : 1.0f;
-            dot[i] = 0.0f;
+        for (int x = 0; x < 4; ++x) {  // 1 KiB: eight rows of 128 bytes
+            const int off = Bytes::at(p, 1, x, wcol, lane);
+            lds_dma16(bytes.rs, off, smine + 8192 + x * 1024);
+            lds_dma16(bytes.rs, off == kOob ? kOob : off + p.hoff, smine + 12288 + x * 1024);
 #pragma unroll
             for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int y = 0; y < WTN / 128; ++y) {
-                    const int gr = (n0 + wn * WTN) / 128 + y;
-                    sc[b][i][y] = m < t.Mg && gr < groups
-                                      ? *reinterpret_cast<const uint32_t *>(
-                                            p.ck_scale + ((static_cast<int64_t>(b) * groups + gr) * p.extent + q.crow + m) * 4)
-                                      : 0x7f7f7f7fu;
-                }
+                *reinterpret_cast<i32x4_t *>(mine + b * 4096 + x * 1024 + lane * 16) = bytes.h[b][x];
         }
-        wait_vmem<0>();
-        __syncthreads();
-        // packed here and now: left to its use behind the barrier, what a pair is made
-        // of would be kept instead, more than the registers hold
+        wave_order();
+        // packed here and now: left to its use, what a pair is made of would be kept
+        // instead, more than the registers hold
         auto pack2 = [](float lo, float hi) {
             const f2_t v = {lo, hi};
             uint32_t u = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf2_t));
             asm volatile("" : "+v"(u));
             return u;
         };
-        uint32_t act[TM][TN][4][2];  // bf16 pairs
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < TM; ++i) {
+            char *const at_i = mine + i * 8192;
+            const int row = lane & 31;
+            float dot = 0.0f;
+            uint32_t act[TN][4][2];  // bf16 pairs
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                const float s1 = ck8_scale((sc[0][i][j / 4] >> (8 * (j % 4))) & 255u);
-                const float s3 = ck8_scale((sc[1][i][j / 4] >> (8 * (j % 4))) & 255u);
+                const float s1 = ck8_scale((bytes.sc[0][i] >> (8 * j)) & 255u);
+                const float s3 = ck8_scale((bytes.sc[1][i] >> (8 * j)) & 255u);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     // four values at a time: spread over more of them, the values between
                     // would not fit the registers
                     __builtin_amdgcn_sched_barrier(0);
                     float a1[4], a3[4], g1[4], g3[4], ac[4];
-                    const int row = wm * WTM + i * 32 + (lane & 31);
-                    const int col = wn * WTN + j * 32 + 8 * g + 4 * (lane >> 5);
-                    const int at = row * BN + 16 * ((col >> 4) ^ (row & 15)) + (col & 15);
-                    ck8_unpack4(*reinterpret_cast<const uint32_t *>(smem + at), s1, a1);
-                    ck8_unpack4(*reinterpret_cast<const uint32_t *>(smem + BM * BN + at), s3, a3);
+                    const int col = j * 32 + 8 * g + 4 * (lane >> 5);
+                    const int at = row * 128 + 16 * ((col >> 4) ^ (row & 7)) + (col & 15);
+                    ck8_unpack4(*reinterpret_cast<const uint32_t *>(at_i + at), s1, a1);
+                    ck8_unpack4(*reinterpret_cast<const uint32_t *>(at_i + 4096 + at), s3, a3);
                     float part = 0.0f;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float v = acc[0][i][j][4 * g + r];
                         const float sg = __builtin_amdgcn_rcpf(1.0f + __expf(-a1[r]));
-                        const float si = a1[r] * sg, va = v * rsc[i];
+                        const float si = a1[r] * sg, va = v * bytes.w[i];
                         ac[r] = si * a3[r];
                         part = __builtin_fmaf(v, ac[r], part);
-                        ac[r] *= rsc[i];
+                        ac[r] *= bytes.w[i];
                         g1[r] = va * a3[r] * sg * (1.0f + a1[r] * (1.0f - sg));
                         g3[r] = va * si;
                     }
                     // columns past N hold other bytes
-                    if (n_lane + j * 32 + 8 * g < p.N) dot[i] += part;
-                    asm volatile("" : "+v"(dot[i]));  // as pack2
+                    if (n_lane + j * 32 + 8 * g < p.N) dot += part;
+                    asm volatile("" : "+v"(dot));  // as pack2
                     acc[0][i][j][4 * g] = __uint_as_float(pack2(g1[0], g1[1]));
                     acc[0][i][j][4 * g + 1] = __uint_as_float(pack2(g1[2], g1[3]));
                     acc[0][i][j][4 * g + 2] = __uint_as_float(pack2(g3[0], g3[1]));
                     acc[0][i][j][4 * g + 3] = __uint_as_float(pack2(g3[2], g3[3]));
-                    act[i][j][g][0] = pack2(ac[0], ac[1]);
-                    act[i][j][g][1] = pack2(ac[2], ac[3]);
+                    act[j][g][0] = pack2(ac[0], ac[1]);
+                    act[j][g][1] = pack2(ac[2], ac[3]);
                 }
             }
-        __syncthreads();  // the ring is free again
-        if (p.ck_dots) {
-            float *const ds = reinterpret_cast<float *>(smem);
-#pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const float v = dot[i] + __shfl_xor(dot[i], 32, 64);
-                if (lane < 32) ds[wn * BM + wm * WTM + i * 32 + lane] = v;
+            if (i == 0) wait_vmem<0>();  // the other rows' bytes, before stores join what is in flight
+            if (p.ck_dots) {
+                dot += __shfl_xor(dot, 32, 64);
+                const int m = m_lane + i * 32;
+                if (lane < 32 && m < t.Mg) p.ck_dots[static_cast<int64_t>(wcol / 128) * p.extent + q.crow + m] = dot;
             }
-            __syncthreads();
-            for (int r = threadIdx.x; r < BM; r += NT) {
-                float v = ds[r];
+            auto out = [&](auto stream) {
 #pragma unroll
-                for (int w = 1; w < WGN; ++w) v += ds[w * BM + r];
-                if (m0 + r < t.Mg) p.ck_dots[static_cast<int64_t>(t.nt) * p.extent + q.crow + m0 + r] = v;
-            }
-            __syncthreads();
-        }
-        __bf16 *const cs = reinterpret_cast<__bf16 *>(smem);
-        for (int o = 0; o < 3; ++o) {
-            const int64_t ld = o == 2 ? p.N : p.ldc;
-            __bf16 *const dst = static_cast<__bf16 *>(o == 2 ? p.ck_act : p.C0) + q.crow * ld + (o == 1 ? p.hoff : 0);
-            for (int pass = 0; pass < kPass; ++pass) {
-                if (kPass == 1 || wm == pass) {
+                for (int o = 0; o < 3; ++o) {
+                    const int64_t ld = o == 2 ? p.N : p.ldc;
+                    __bf16 *const dst = static_cast<__bf16 *>(o == 2 ? p.ck_act : p.C0) + (q.crow + wrow + i * 32) * ld +
+                                        (o == 1 ? p.hoff : 0) + wcol;
+                    wave_order();  // what was here has been read
 #pragma unroll
-                    for (int i = 0; i < TM; ++i)
+                    for (int j = 0; j < TN; ++j)
 #pragma unroll
-                        for (int j = 0; j < TN; ++j)
+                        for (int g = 0; g < 4; ++g) {
+                            const int c8 = j * 4 + g;
+                            const f32x16_t &v = acc[0][i][j];
+                            *reinterpret_cast<uint2 *>(at_i + row * 256 + 16 * (c8 ^ (row & 15)) + 8 * (lane >> 5)) =
+                                o == 2 ? make_uint2(act[j][g][0], act[j][g][1])
+                                       : make_uint2(__float_as_uint(o ? v[4 * g + 2] : v[4 * g]),
+                                                    __float_as_uint(o ? v[4 * g + 3] : v[4 * g + 1]));
+                        }
+                    wave_order();
 #pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                const int row = (kPass == 1 ? wm * WTM : 0) + i * 32 + (lane & 31);
-                                const int col = wn * WTN + j * 32 + 8 * g + 4 * (lane >> 5);
-                                const f32x16_t &v = acc[0][i][j];
-                                *reinterpret_cast<uint2 *>(cs + row * LDC + col) =
-                                    o == 2 ? make_uint2(act[i][j][g][0], act[i][j][g][1])
-                                           : make_uint2(__float_as_uint(o ? v[4 * g + 2] : v[4 * g]),
-                                                        __float_as_uint(o ? v[4 * g + 3] : v[4 * g + 1]));
-                            }
+                    for (int x = 0; x < 8; ++x) {
+                        const int r = 4 * x + lane / 16, c8 = lane & 15;
+                        const i32x4_t v = *reinterpret_cast<const i32x4_t *>(at_i + r * 256 + 16 * (c8 ^ (r & 15)));
+                        if (wrow + i * 32 + r < t.Mg && wcol + 8 * c8 < p.N) {
+                            i32x4_t *const d = reinterpret_cast<i32x4_t *>(dst + r * ld + 8 * c8);
+                            if constexpr (decltype(stream)::value) __builtin_nontemporal_store(v, d);
+                            else *d = v;
+                        }
+                    }
                 }
-                __syncthreads();
-#pragma unroll 4
-                for (int c = threadIdx.x; c < RP * BN / 8; c += NT) {
-                    const int row = c / (BN / 8), c8 = c % (BN / 8);
-                    const int m = m0 + pass * RP + row, n = n0 + 8 * c8;
-                    if (m < t.Mg && n < p.N)
-                        *reinterpret_cast<uint4 *>(dst + m * ld + n) = *reinterpret_cast<const uint4 *>(cs + row * LDC + 8 * c8);
-                }
-                if (o + 1 < 3 || pass + 1 < kPass) __syncthreads();
-            }
+            };
+            if (p.ck_stream) out(std::true_type{});
+            else out(std::false_type{});
         }
         return;
     }
@@ -1107,6 +1141,8 @@ void gemm_dma_kernel(GemmArgs p) {
     const int nph = p.group_mode == GM_KSPLIT ? 1 : p.nphase;
     const int total = t.Kg > kstart ? ktiles * nph : 0;
 
+    std::conditional_t<EPI == EPI_SWIGLU_BWD_CK8, BackBytes, NoBytes> bytes;
+    bytes.load(p, t, q, m0 + wm * (BM / WGM), n0 + wn * (BN / WGN), lane);
     PA pa;
     PB pb;
     const bool amap = A_KC && p.a_map != nullptr && p.group_mode == GM_ROWS;
@@ -1327,7 +1363,7 @@ void gemm_dma_kernel(GemmArgs p) {
     if (wact) k_loop(std::true_type{});
     else k_loop(std::false_type{});
     wait_vmem<0>();  // no load may still target LDS when the block ends
-    gemm_epilogue<BM, BN, WGM, WGN, NB, S * kStage, EPI, OutT>(p, t, q, acc, smem, sbase, m0, n0, lane, wave);
+    gemm_epilogue<BM, BN, WGM, WGN, NB, S * kStage, EPI, OutT>(p, t, q, acc, smem, sbase, m0, n0, lane, wave, bytes);
 }
 
 template <int BM, int BN, int BK, int WGM, int WGN, int NB, bool A_KC, bool B_KC, int S, int EPI, typename OutT,
