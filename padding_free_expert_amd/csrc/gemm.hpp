@@ -1379,20 +1379,28 @@ inline hipError_t launch_gemm_dma(const GemmArgs &p, hipStream_t stream) {
 
 // ------------------------------------------------------------- fp32 path
 //
-// Plain FMA tiles (64x64 per block, 4x4 per thread).  Every output is summed
+// Plain FMA tiles (64x64 per block, 4x4 per thread, or 32x64).  Every output is summed
 // in ascending k with one fused multiply-add per term, so the fp32 router's
 // logits follow exactly that order.
-
-// A step's values are asked for a step ahead and pass through registers into the other of
-// two shared tiles: one barrier a step, under the products.  An operand's 16 k by 64 rows
-// (or columns) are read in its memory's order, whole 64-byte pieces (2400 rows of 32
-// experts, d = 448, h = 136, up: 147 -> 81 us; the sums and their order are the same).
+//
+// A step's values are asked for two steps ahead and pass through registers into one of two
+// shared tiles: one barrier a step, under the products.  An operand's 16 k by 64 rows (or
+// columns) are read in its memory's order, whole 64-byte pieces.  Bound by the vector
+// units where there are many blocks (8192 rows of 16 experts, d = 1024, h = 704: up 385 us,
+// 61 TFLOP/s), else by each step's chain of load, store, barrier and reads (2400 rows of 32
+// experts, d = 448, h = 136, up: 46 us).  The tile's height goes by the grid, see
+// launch_gemm_f32; on the lower one the reads of a step are all under way at once, at 226
+// registers (two matrices; by twos 99 -> 81 us at 80 rows of 8 experts, d = 1024), which
+// with many blocks cost more than the waits (385 -> 701).
 // The product behind 8-bit pre-activations keeps sums of 128 k and adds them up (FOLD):
 // its gates' gradients are dot products of whole rows, and one chain of d terms costs
 // them twice the error.
-template <int NB, bool A_KC, bool B_KC, int EPI>
+template <int BM, int NB, bool A_KC, bool B_KC, int EPI>
 __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs p) {
-    constexpr int BM = 64, BN = 64, BK = 16;
+    constexpr int BN = 64, BK = 16, R = BM / 16;  // rows of a thread
+    constexpr int AE = BM * BK / 256;             // elements of A it loads
+    typedef float row_t __attribute__((ext_vector_type(R)));
+    typedef float f4_t __attribute__((ext_vector_type(4)));
     // rows of 68: a 16-byte read stays aligned, and a k-major write (16 k by 4 rows or
     // columns) meets all 64 banks once
     __shared__ __align__(16) float As[2][BK][BM + 4];
@@ -1402,15 +1410,15 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs p) {
     const GroupPtrs<float> q = group_ptrs<float>(p, t);
     const int m0 = t.m0, n0 = t.nt * BN;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[NB][4][4];
+    float acc[NB][R][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[b][i][j] = 0.0f;
     constexpr bool FOLD = EPI == EPI_SWIGLU_BWD_CK8;
-    float sum[FOLD ? NB : 1][4][4] = {};
+    float sum[FOLD ? NB : 1][R][4] = {};
     const int nph = (p.group_mode == GM_ROWS) ? p.nphase : 1;
     const int steps = (t.Kg + BK - 1) / BK, total = steps * nph;
     // element i of this thread: (k, row) of A, (k, column) of B
@@ -1418,57 +1426,64 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs p) {
     auto am = [&](int i) { const int e = threadIdx.x + 256 * i; return A_KC ? e / BK : e % BM; };
     auto bk = [&](int i) { const int e = threadIdx.x + 256 * i; return B_KC ? e % BK : e / BN; };
     auto bn = [&](int i) { const int e = threadIdx.x + 256 * i; return B_KC ? e / BK : e % BN; };
-    float ra[4], rb[NB][4];
-    auto fetch = [&](int step) {
-        const int ph = step / steps, k0 = (step - ph * steps) * BK;
-        const float *A = ph ? q.A1 : q.A0;
-        const float *B0 = ph ? q.B1 : q.B0;
+    // Where they lie, but for the step.  What is not there (rows, columns, k behind the
+    // end) is read as the operand's first element and counts as zero: without branches
+    // around them the loads can be waited for by their number.
+    const bool mapped_m = A_KC && p.a_map && p.group_mode == GM_ROWS;
+    const bool mapped_k = !A_KC && p.a_map && p.group_mode == GM_KSPLIT;
+    int64_t aoff[AE], boff[4];
+    bool aok[AE], bok[4];
+#pragma unroll
+    for (int i = 0; i < AE; ++i) {
+        const int gm = m0 + am(i);
+        aok[i] = gm < t.Mg;
+        aoff[i] = A_KC ? (mapped_m && aok[i] ? p.a_map[t.base + gm] : gm) * p.lda + ak(i) : mapped_k ? gm : ak(i) * p.lda + gm;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int gn = n0 + bn(i);
+        bok[i] = gn < p.N;
+        boff[i] = B_KC ? gn * p.ldb + bk(i) : bk(i) * p.ldb + gn;
+    }
+    float ra[2][AE], rb[2][NB][4];  // of an even and an odd step
+    auto fetch = [&](int step, float (&fa)[AE], float (&fb)[NB][4]) {
+        const int ph = step >= steps ? 1 : 0, k0 = (step - ph * steps) * BK;
+        const float *const A0 = mapped_m || mapped_k ? static_cast<const float *>(p.A0) : ph ? q.A1 : q.A0;
+        const float *const B0 = ph ? q.B1 : q.B0;
+        const int64_t astep = A_KC ? k0 : mapped_k ? 0 : k0 * p.lda, bstep = B_KC ? k0 : k0 * p.ldb;
+#pragma unroll
+        for (int i = 0; i < AE; ++i) {
+            const bool ok = aok[i] && k0 + ak(i) < t.Kg;
+            const int64_t row = mapped_k && ok ? p.a_map[t.base + k0 + ak(i)] * p.lda : 0;
+            fa[i] = A0[ok ? aoff[i] + row + astep : 0];
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int gm = m0 + am(i), gk = k0 + ak(i);
-            float va = 0.0f;
-            if (gm < t.Mg && gk < t.Kg) {
-                if (A_KC && p.a_map && p.group_mode == GM_ROWS)
-                    va = static_cast<const float *>(p.A0)[static_cast<int64_t>(p.a_map[t.base + gm]) * p.lda + gk];
-                else if (!A_KC && p.a_map && p.group_mode == GM_KSPLIT)
-                    va = static_cast<const float *>(p.A0)[static_cast<int64_t>(p.a_map[t.base + gk]) * p.lda + gm];
-                else
-                    va = A_KC ? A[static_cast<int64_t>(gm) * p.lda + gk] : A[static_cast<int64_t>(gk) * p.lda + gm];
-            }
-            ra[i] = va;
-            const int gn = n0 + bn(i), gkb = k0 + bk(i);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                float vb = 0.0f;
-                const float *Bm = b ? q.Bx : B0;
-                if (gn < p.N && gkb < t.Kg)
-                    vb = B_KC ? Bm[static_cast<int64_t>(gn) * p.ldb + gkb] : Bm[static_cast<int64_t>(gkb) * p.ldb + gn];
-                rb[b][i] = vb;
-            }
+            const int64_t off = bok[i] && k0 + bk(i) < t.Kg ? boff[i] + bstep : 0;
+            fb[0][i] = B0[off];
+            if constexpr (NB == 2) fb[1][i] = q.Bx[off];
         }
     };
-    if (total > 0) fetch(0);
-    for (int step = 0; step < total; ++step) {
-        const int s = step & 1;
+    auto run_step = [&](int step, float (&fa)[AE], float (&fb)[NB][4]) {
+        const int s = step & 1, kleft = t.Kg - (step >= steps ? step - steps : step) * BK;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            As[s][ak(i)][am(i)] = ra[i];
+        for (int i = 0; i < AE; ++i) As[s][ak(i)][am(i)] = aok[i] && ak(i) < kleft ? fa[i] : 0.0f;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) Bs[s][b][bk(i)][bn(i)] = rb[b][i];
-        }
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) Bs[s][b][bk(i)][bn(i)] = bok[i] && bk(i) < kleft ? fb[b][i] : 0.0f;
         __syncthreads();  // the tile is whole; the other one's readers are past the barrier before
-        if (step + 1 < total) fetch(step + 1);
-#pragma unroll
+        if (step + 2 < total) fetch(step + 2, fa, fb);
+#pragma unroll(BM == 32 ? BK : 2)
         for (int kk = 0; kk < BK; ++kk) {
-            typedef float f4_t __attribute__((ext_vector_type(4)));
-            const f4_t a = *reinterpret_cast<const f4_t *>(&As[s][kk][ty * 4]);
+            const row_t a = *reinterpret_cast<const row_t *>(&As[s][kk][ty * R]);
             f4_t bv[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) bv[b] = *reinterpret_cast<const f4_t *>(&Bs[s][b][kk][tx * 4]);
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < R; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[b][i][j] = __builtin_fmaf(a[i], bv[b][j], acc[b][i][j]);
         }
@@ -1477,7 +1492,7 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs p) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < R; ++i)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             sum[b][i][j] += acc[b][i][j];
@@ -1485,12 +1500,18 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs p) {
                         }
             }
         }
+    };
+    if (total > 0) fetch(0, ra[0], rb[0]);
+    if (total > 1) fetch(1, ra[1], rb[1]);
+    for (int step = 0; step < total; step += 2) {
+        run_step(step, ra[0], rb[0]);
+        if (step + 1 < total) run_step(step + 1, ra[1], rb[1]);
     }
     if constexpr (FOLD) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < R; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[b][i][j] += sum[b][i][j];
     }
@@ -1498,8 +1519,8 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs p) {
         // a thread's four columns lie in one block of 32, the eight threads tx ^ 0..7 hold it
         const int groups = (p.N + 127) / 128, n = n0 + tx * 4, blk = n / 32;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = m0 + ty * 4 + i;
+        for (int i = 0; i < R; ++i) {
+            const int m = m0 + ty * R + i;
             const int64_t row = q.crow + m;
             const bool live = m < t.Mg && n < p.N;
             uint8_t *const sc = p.ck_scale + (static_cast<int64_t>(blk / 4) * p.extent + row) * 4 + blk % 4;
@@ -1564,20 +1585,28 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs p) {
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
+            const int m = m0 + ty * R + i, n = n0 + tx * 4 + j;
             if (m < t.Mg && n < p.N)
                 epilogue<EPI, float>(p, q.crow, q.coff, m, n, acc[0][i][j], acc[NB - 1][i][j]);
         }
 }
 
+// Tiles of 64 rows from which these are taken, two for each compute unit; below it 32 rows
+// (184 tiles: 132 -> 103 us with them, 1584 tiles: 397 -> 459).
+constexpr int64_t kF32Blocks = 512;
+
 template <int NB, bool A_KC, bool B_KC, int EPI>
 inline hipError_t launch_gemm_f32(const GemmArgs &p, hipStream_t stream) {
     const int64_t grid = gemm_grid<64, 64>(p);
     if (grid <= 0) return hipSuccess;
-    hipLaunchKernelGGL((gemm_f32_kernel<NB, A_KC, B_KC, EPI>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, p);
+    if (grid < kF32Blocks)
+        hipLaunchKernelGGL((gemm_f32_kernel<32, NB, A_KC, B_KC, EPI>), dim3(static_cast<unsigned>(gemm_grid<32, 64>(p))),
+                           dim3(256), 0, stream, p);
+    else
+        hipLaunchKernelGGL((gemm_f32_kernel<64, NB, A_KC, B_KC, EPI>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
