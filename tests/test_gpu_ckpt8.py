@@ -414,3 +414,36 @@ def test_layer_refuses(xm):
     for kw in (dict(ckpt8=True, lean=True), dict(ckpt8=True, backward=False)):
         with pytest.raises(ValueError, match="ckpt8"):
             _layer(wl, **kw)
+
+
+@pytest.mark.parametrize("counts", [[34000], [17000, 120, 16880], [150] * 227])
+def test_results_past_the_caches_are_those_of_parts(xm, counts):
+    """Results of more than 256 MB take another way to memory: the same bits as calls on
+    the single experts' rows, whose results do not (every expert alone for the ends, the
+    last rows of a segment among them)."""
+    d, h, off = 32, 1368, _offsets(counts)
+    R, E = off[-1], len(counts)
+    assert R * h * 6 > 2 ** 28
+    g = _gen(9)
+    dy = torch.randn((R, d), device="cuda", generator=g).to(BF)
+    w2 = (torch.randn((E, h, d), device="cuda", generator=g) * h ** -0.5).to(BF)
+    hq = torch.randint(-127, 128, (R, 2 * h), device="cuda", generator=g, dtype=I8)
+    hs = torch.randint(118, 124, xm.ckpt8_scale_shape(R, h), device="cuda", generator=g, dtype=U8)
+    wt = torch.rand((R,), device="cuda", generator=g)
+
+    def run(r0, r1, e0, e1):
+        n = r1 - r0
+        o = torch.tensor([v - r0 for v in off[e0:e1 + 1]], dtype=I32, device="cuda") if e1 - e0 > 1 else \
+            torch.tensor([0, n], dtype=I32, device="cuda")
+        dh, act = torch.full((n, 2 * h), 3.0, dtype=BF, device="cuda"), torch.full((n, h), 3.0, dtype=BF, device="cuda")
+        dw = torch.full((n,), 3.0, device="cuda")
+        xm.xmoe_expert_ffn_bwd_dact_ckpt8(dy[r0:r1], w2[e0:e1], hq[r0:r1], hs[:, :, r0:r1].contiguous(), o, dh, act,
+                                          row_weights=wt[r0:r1], dweights=dw)
+        return dh, act, dw
+
+    whole = run(0, R, 0, E)
+    for e in sorted({0, E // 2, E - 1}):
+        for r0 in range(off[e], off[e + 1], 8192):
+            r1 = min(r0 + 8192, off[e + 1])
+            for a, b in zip(whole, run(r0, r1, e, e + 1)):
+                assert torch.equal(a[r0:r1], b), (e, r0)
