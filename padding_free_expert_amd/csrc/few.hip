@@ -18,12 +18,12 @@
 // Bound by the weights' bytes, which a plain read of as much takes 7 TB/s for (1 GB; 64 MB
 // 5.9, 24 MB 4.5, launches in a row), and for one token by four launches' starts and the
 // waits from one to the next.  Measured (d = 2048, 64 experts of h = 1408, top-6, two
-// shared; bf16 / 8-bit weights; the layer's sequence in brackets): 1 token 40 / 36 us (118
-// / 114, for 138 and 71 MB), 4 88 / 61 (148 / 111), 16 179 / 113 (230 / 128), 64 223 / 137 us
-// (252 / 142, for 1.1 and 0.57 GB).  64 tokens on 160 experts of d = 4096, h = 1024, top-8
-// 652 us (758), of which the up-projection is 408: 6.6 TB/s.  With 8-bit weights and few
-// experts the sequence wins from 32 tokens on (8 experts, top-2: 44 against 57 us at 32
-// tokens, 63 against 56 at 64).
+// shared; bf16 / 8-bit weights; the layer's sequence in brackets): 1 token 41 / 36 us (118
+// / 130, for 138 and 71 MB), 4 85 / 60 (146 / 127), 16 169 / 107 (228 / 129), 64 224 / 137 us
+// (253 / 141, for 1.1 and 0.57 GB).  64 tokens on 160 experts of d = 4096, h = 1024, top-8
+// 664 us, of which the up-projection is 409: 6.3 TB/s.  With 8-bit weights and few
+// experts the sequence wins from about 32 tokens on (16 experts, top-4: 55 against 59 us at
+// 16 tokens, 62 against 59 at 32, 79 against 62 at 64).
 //
 // A block's row tiles (one of 16 rows, or two) are a template argument, and which of the
 // two instances runs is decided in front of its loop: with a branch around the second
