@@ -649,7 +649,8 @@ xmoe_status xmoe_expert_ffn_down_mx8(const void *act, const void *act_scale, con
  *   y[t]   = sum_j topk_w[t,j] * (a[t,j] . w2[e])  (+ the shared experts' FFN of x[t])
  * fp32 sums; y is rounded once, at the end: a is not rounded to the dtype on the way
  * (bf16: held as the sum of two bf16 values, within 2^-16 of it), nor the experts'
- * outputs, as xmoe_expert_ffn_up and _down do.  The sums run
+ * outputs, as xmoe_expert_ffn_up and _down do (an infinity in w2 or s2 may then
+ * come out as a NaN).  The sums run
  * in another order than xmoe_route's and xmoe_expert_ffn_up's, so that results
  * agree to rounding, and experts whose selection values differ by less than that
  * may be chosen the other way round.  Whatever the logits hold, a token's ids are
