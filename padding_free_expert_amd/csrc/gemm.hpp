@@ -727,7 +727,9 @@ __device__ __forceinline__ void gemm_epilogue(const GemmArgs &p, const Tile &t, 
         // d = 4096, 160 experts, h = 1024 991 TFLOP/s; without H1 and H3 352 and 1033, with
         // them in bf16 372 and 997).  A lane holds 16 of the 32 columns of
         // product (i, j) for its row, lane ^ 32 the others: a scale block is one
-        // product's row, and its columns past N are zeros, which change nothing.
+        // product's row.  The columns past N of a block that N ends in are products with
+        // zeros: they change no scale, being zeros, or NaNs where the row of A is not finite
+        // and the others are not either.
         constexpr int LDC = BN + 8, LDQ = BN + 8;
         constexpr int kPass = BM * LDC * 2 <= RING ? 1 : WGM;
         constexpr int RP = BM / kPass;
@@ -755,7 +757,9 @@ __device__ __forceinline__ void gemm_epilogue(const GemmArgs &p, const Tile &t, 
                                 for (int r = 0; r < 16; ++r)
                                     a = max(a, __float_as_uint(acc[o == 2][i][j][r]) & 0x7fffffffu);
                                 a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), 32, 64)));
-                                const uint32_t b = ck8_scale_byte(a);
+                                // a block past N is 127, also where the row of A is not finite
+                                // (its products with the zeros there are NaNs)
+                                const uint32_t b = n0 + wn * WTN + j * 32 < p.N ? ck8_scale_byte(a) : 127u;
                                 bytes |= b << (8 * j);
                                 inv = ck8_inv_scale(b);
                             }
@@ -1534,13 +1538,13 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs p) {
 #pragma unroll
                     for (int off = 1; off < 8; off <<= 1)
                         a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), off, 64)));
-                    const uint32_t byte = ck8_scale_byte(a);
+                    const uint32_t byte = blk * 32 < p.N ? ck8_scale_byte(a) : 127u;
                     const float *v = acc[b * (NB - 1)][i];
                     if (live)
                         *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.aux_out) + row * p.ld_aux + b * p.hoff + n) =
                             ck8_pack4(v[0], v[1], v[2], v[3], ck8_inv_scale(byte));
-                    // blocks behind N in the last group too: their values are zeros; a
-                    // last tile in the group's first half fills the second
+                    // blocks behind N in the last group too (127 whatever the row of A
+                    // holds); a last tile in the group's first half fills the second
                     if (m < t.Mg && tx % 8 == 0) {
                         sc[b * half] = static_cast<uint8_t>(byte);
                         if (n0 + BN >= p.N && blk % 4 < 2) sc[b * half + 2] = 127;
