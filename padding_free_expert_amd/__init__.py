@@ -175,12 +175,16 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
-def _dt(t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
+def _dtype(dtype: torch.dtype) -> int:
+    if dtype == torch.bfloat16:
         return XMOE_BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return XMOE_F32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    raise TypeError(f"unsupported dtype {dtype}")
+
+
+def _dt(t: torch.Tensor) -> int:
+    return _dtype(t.dtype)
 
 
 def _grad_dt(*grads: torch.Tensor) -> int:
@@ -842,7 +846,7 @@ def xmoe_expert_ffn_down_mx8(act, act_scale, w2, w2_scale, expert_offsets, ye, s
 
 
 def xmoe_layer_few_workspace_size(T: int, d: int, E: int, k: int, h: int, hs: int, dtype) -> int:
-    return int(_lib_few_ws(T, d, E, k, h, hs, XMOE_BF16 if dtype == torch.bfloat16 else XMOE_F32))
+    return int(_lib_few_ws(T, d, E, k, h, hs, _dtype(dtype)))
 
 
 def xmoe_layer_few_mx8_workspace_size(T: int, d: int, E: int, k: int, h: int, hs: int) -> int:
