@@ -355,6 +355,8 @@ class PaddingFreeMoE:
     def backward(self, dy: torch.Tensor, stream=None, hook=None, dloss=None) -> torch.Tensor:
         """dloss: upstream gradient of the balance loss, fp32 [1] on the device
         (None: 1)."""
+        if not self.backward_enabled:
+            raise RuntimeError("this layer has no backward (backward=False)")
         w = self.w
         mark = hook or (lambda name: None)
         _need(dy, (self.T, self.d), (self.dtype,), "dy", self.device)

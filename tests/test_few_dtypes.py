@@ -22,3 +22,12 @@ def test_layer_refuses_weights_of_other_types(dt):
     w = dict(wg=e(64, 8), w1=e(8, 64, 32), w3=e(8, 64, 32), w2=e(8, 32, 64))
     with pytest.raises(TypeError, match="dtype"):
         PaddingFreeMoE(w, 4, 2, backward=False, few=True)
+
+
+def test_a_layer_for_few_tokens_has_no_backward():
+    from padding_free_expert_amd.layer import PaddingFreeMoE
+    e = lambda *s: torch.empty(s, dtype=torch.bfloat16)
+    w = dict(wg=e(64, 8), w1=e(8, 64, 32), w3=e(8, 64, 32), w2=e(8, 32, 64))
+    layer = PaddingFreeMoE(w, 4, 2, backward=False, few=True)
+    with pytest.raises(RuntimeError, match="no backward"):
+        layer.backward(e(4, 64))
