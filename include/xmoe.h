@@ -642,8 +642,10 @@ xmoe_status xmoe_expert_ffn_down_mx8(const void *act, const void *act_scale, con
 /* ------------------------------------------------------------------------
  * The whole layer for a few tokens (0 <= T <= 64), forward only: gate, top-k,
  * experts, shared experts and combine in one call, for the next tokens of a few
- * sequences.  The weights that the tokens chose are read once; no Padding-Free
- * Token buffer is built.
+ * sequences.  The weights that the tokens chose are read once for every 16 rows of
+ * an expert (32 with more than 8 rows an expert on average and more than 16 tokens);
+ * no Padding-Free Token buffer is built.  For tokens that meet on a few experts, 64
+ * rows each, the layer's sequence of calls is faster.
  *   logits, topk_ids, topk_w : as xmoe_route
  *   a[t,j] = silu(x[t] . w1[e]) * (x[t] . w3[e]),  e = topk_ids[t,j]
  *   y[t]   = sum_j topk_w[t,j] * (a[t,j] . w2[e])  (+ the shared experts' FFN of x[t])

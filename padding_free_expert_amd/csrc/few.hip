@@ -3,8 +3,9 @@
 //
 // The layer's other path sorts rows by expert and multiplies 128-row tiles; with a
 // token or two for each expert its time is launches, searches for tiles and rows that
-// are not there.  Here the weights that the tokens chose are streamed past their rows
-// once, and what one product leaves for the next stays in the caches:
+// are not there.  Here the weights that the tokens chose are streamed past their rows,
+// once for each 16 (or 32) rows of an expert, and what one product leaves for the next
+// stays in the caches:
 //   1  partial logits of the gate, and the shared experts' H1, H3 (they need no
 //      routing): K split over blocks
 //   2  softmax and top-k, a wave for each token (up to four tokens: at the start of 3)
@@ -17,20 +18,25 @@
 //
 // Bound by the weights' bytes, which a plain read of as much takes 7 TB/s for (1 GB; 64 MB
 // 5.9, 24 MB 4.5, launches in a row), and for one token by four launches' starts and the
-// waits from one to the next.  Measured (d = 2048, 64 experts of h = 1408, top-6, two
-// shared; bf16 / 8-bit weights; the layer's sequence in brackets): 1 token 41 / 36 us (118
-// / 130, for 138 and 71 MB), 4 85 / 60 (146 / 127), 16 169 / 107 (228 / 129), 64 224 / 137 us
-// (253 / 141, for 1.1 and 0.57 GB).  64 tokens on 160 experts of d = 4096, h = 1024, top-8
-// 664 us, of which the up-projection is 409: 6.3 TB/s.  With 8-bit weights and few
-// experts the sequence wins from about 32 tokens on (16 experts, top-4: 55 against 59 us at
-// 16 tokens, 62 against 59 at 32, 79 against 62 at 64).
+// waits from one to the next.  Measured as layers, replayed from a graph (d = 2048, 64
+// experts of h = 1408, top-6, two shared; bf16 / 8-bit weights behind the norm; the layer's
+// sequence in brackets): 1 token 45 / 39 us (135 / 73, for 138 and 71 MB), 4 90 / 63 (148 /
+// 91), 16 180 / 113 (241 / 133), 64 226 / 139 us (259 / 148, for 1.1 and 0.57 GB).  64 tokens
+// on 160 experts of d = 4096, h = 1024, top-8 658 us (762), of which the up-projection is
+// 409: 6.3 TB/s.
+// The sequence wins where experts have many rows: with 8-bit weights and few experts from
+// about 32 tokens on (16 experts, top-4: 55 against 61 us at 16 tokens, 62 against 62 at 32,
+// 78 against 65 at 64), with bf16 where 64 tokens take every expert (16 experts of 64 rows:
+// 188 against 143; 8 experts: 99 against 110), and by far where many tokens meet on a few
+// experts of many (64 tokens on 8 of those 160: 608 against 218 us; 12 tokens on them: 83
+// against 211), since further passes over a part's weights come from memory again.
 //
 // A block's row tiles (one of 16 rows, or two) are a template argument, and which of the
 // two instances runs is decided in front of its loop: with a branch around the second
 // tile's products hipcc leaves too few waits between a matrix instruction and the copy of
 // its result that a branch jumps to (ROCm 7.2, fp32: four columns of 64 were wrong).
-// Two tiles at a time where experts have more than 16 rows; else more rows take another
-// pass over the part's weights, which the caches hold by then.
+// Two tiles at a time where experts have more than 8 rows on average (see make_plan).  An
+// expert with more rows than that takes further passes over its weights.
 //
 // Products: the weights are the first operand of the matrix instruction (16 columns),
 // the rows the second (16 rows), so that a row costs nothing up to 16 of them and rows
@@ -54,16 +60,21 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kFewWaves = 4;
 constexpr int kFewThreads = 64 * kFewWaves;
-// Weights pass the caches by: nothing reads them again soon (64 tokens on 160 experts 665
-// -> 730 us without, one token 49 -> 52).
+// Weights pass the caches by: with an even choice of experts nothing reads them again soon
+// (64 tokens on 160 experts 650 -> 716 us without, in 8 bits 372 -> 415).  All 64 on the
+// same 8 of them, four passes over the same weights, would gain from the caches (671 ->
+// 505 us, in 8 bits 279 -> 232).
 constexpr int kNt = 2;
-// Blocks that a small launch is cut into (640: one token 41 -> 46 us, two on a compute unit
-// being all that run at once; 384: 12 small fp32 experts 29 -> 32), and one of long parts
-// (2048: 4 tokens of 32 8-bit experts 237 -> 245 us, 1280: 12 tokens 112.5 -> 117).
+// Blocks that a small launch is cut into: two on a compute unit, where four would fit (384,
+// 512, 640, 1024: one token in bf16 42.9, 41.8, 43.7, 42.4 us, in 8 bits 36.1, 34.5, 34.9,
+// 34.9; 5 fp32 tokens of 30 experts 34.4, 31.2, 31.3, 31.2), and one of long parts (2048:
+// 4 tokens of 32 8-bit experts 237 -> 245 us, 1280: 12 tokens 112.5 -> 117).
 constexpr int kFewBlocks = 512, kBlocks = 1536;
 constexpr int kGateParts = 16;    // of the gate's sums: what the top-k reads for each logit
 constexpr int kPartRows = 16;     // see make_plan
-constexpr int kManyStrips = 2048; // strips from which each is a wave's own (see few_down_kernel)
+// Strips (times parts) from which each is a wave's own (see few_down_kernel): 64 tokens of 64
+// bf16 experts, 3072 of them, 207 us so and 215 by blocks, 12 tokens of them 149 and 151.
+constexpr int kManyStrips = 2048;
 // Tokens and slots whose top-k the up-projection's blocks find themselves: a wave for each
 // token, no launch (4.5 us) between the gate and the experts.
 constexpr int kInlineTokens = kFewWaves, kInlineSlots = 64;
@@ -551,7 +562,8 @@ __device__ __forceinline__ void up_unit(const FewArgs &p, const FewFfn &f, int e
 
 // ------------------------------------------------------------------- kernels
 
-// waves a SIMD that the registers are kept for
+// Waves a SIMD that the registers are kept for (bf16's down-projection with two row tiles
+// has 66 KB of shared memory and runs two blocks on a compute unit, two waves a SIMD)
 constexpr int few_occ(int row_tiles) { return row_tiles == 1 ? 4 : 3; }
 
 // 1: the gate's blocks first (what follows waits for them), then the shared experts'
@@ -826,7 +838,7 @@ __global__ __launch_bounds__(64) void few_topk_kernel(FewArgs p) {
 // 4: the chosen experts' units first, then the shared ones'.  WK = 4: the waves split a
 // part's steps and meet after each strip; WK = 1: a wave takes every fourth strip over the
 // whole part and stores its sums, for launches with more strips than waves that run at once
-// (112 8-bit experts of 768 x 2048 with two rows each: 65 -> 40 us, 4.5 TB/s, the meetings'
+// (112 8-bit experts of 768 x 2048 with two rows each: 65 -> 43 us, 4.3 TB/s, the meetings'
 // waits being gone)
 template <class C, int MT, int KP, int WK>
 __global__ __launch_bounds__(kFewThreads, few_occ(MT)) void few_down_kernel(FewArgs p, int units) {
@@ -1011,6 +1023,8 @@ Plan make_plan(const FewSizes &z, char *ws) {
     pl.own_topk = !(a.T <= kInlineTokens && a.T * a.k <= kInlineSlots && a.E <= 256);
     // two row tiles at a time: the tokens of the gate and of the shared experts'
     // up-projection, and the chosen experts' rows where they have more than 8 on average
+    // (12.8 rows: 232 us so and 262 by single tiles in bf16, 107 and 118 in 8 bits, 162 and
+    // 189 in fp32; 5 to 8 rows: level, 302 to 306 in bf16; 24 tokens of 9 rows 81 and 74)
     pl.tokens2 = a.T > 16;
     pl.rows2 = pl.tokens2 && static_cast<int64_t>(a.T) * a.k > 8 * static_cast<int64_t>(a.E);
     const int64_t units = std::min<int64_t>(static_cast<int64_t>(a.T) * a.k, a.E), slots = static_cast<int64_t>(a.T) * a.k;
@@ -1023,7 +1037,9 @@ Plan make_plan(const FewSizes &z, char *ws) {
         // Every strip of the down-projection reads the parts of its rows, a part costing as
         // much as 1 / 64 of the weights for each row of an expert: with many rows the
         // activations are formed before, the shared experts' by the top-k's launch, if there
-        // is one, the chosen experts' by one of their own
+        // is one, the chosen experts' by one of their own.  Where the chosen ones' border
+        // lies, by cap, 2 cap and 4 cap: 40 bf16 experts of 13 rows 235, 235, 247 us; 16
+        // 8-bit experts of 8 rows 34.4, 33.4, 36.2, but of 16 rows 66, 77, 77
         const int cap = std::max(1, static_cast<int>(kPartRows * units_busy / rows));
         split(z.d, units_busy * hs * up_rows, 2 * C::STEP, C::kLeast, 1 << 30, 1 << 30, &f.up_parts, &f.up_len);
         const bool own_act = routed ? f.up_parts > 2 * cap : pl.own_topk;
@@ -1048,7 +1064,9 @@ Plan make_plan(const FewSizes &z, char *ws) {
         if (pl.own_topk) pl.act = static_cast<int64_t>(a.T) * ((z.hs + 255) / 256);  // beside the top-k
     }
     // Launches with more strips than the compute units' waves take at once: a wave a strip,
-    // and several of them a block, whose activations are formed once for all
+    // and several of them a block, whose activations are formed once for all.  Two strips a
+    // wave from 8192 on, within 5% of one strip on either side (3072 of bf16 207 us with
+    // one, 212 with two; 6144 of 8 bits 128 and 122; 14336 255 and 257; 114688 1686 and 1673)
     const int64_t strips = pl.down + pl.down_shared;
     pl.wave_strips = strips >= kManyStrips;
     a.r.down_strips = pl.wave_strips ? kFewWaves * (strips >= 4 * kManyStrips ? 2 : 1) : 1;

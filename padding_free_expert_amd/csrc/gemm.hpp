@@ -1395,7 +1395,7 @@ inline hipError_t launch_gemm_dma(const GemmArgs &p, hipStream_t stream) {
 // experts, d = 448, h = 136, up: 46 us).  The tile's height goes by the grid, see
 // launch_gemm_f32; on the lower one the reads of a step are all under way at once, at 226
 // registers (two matrices; by twos 99 -> 81 us at 80 rows of 8 experts, d = 1024), which
-// with many blocks cost more than the waits (385 -> 701).
+// with many blocks cost more than the waits (529 us on these tiles for the 385).
 // The product behind 8-bit pre-activations keeps sums of 128 k and adds them up (FOLD):
 // its gates' gradients are dot products of whole rows, and one chain of d terms costs
 // them twice the error.
@@ -1598,8 +1598,11 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs p) {
         }
 }
 
-// Tiles of 64 rows from which these are taken, two for each compute unit; below it 32 rows
-// (184 tiles: 132 -> 103 us with them, 1584 tiles: 397 -> 459).
+// Tiles of 64 rows from which these are taken, two for each compute unit; below it 32 rows.
+// With 64 and 32 rows, one matrix: 216 tiles 61 and 37 us, 504 tiles 61 and 47, 693 tiles
+// 67 and 74, 1584 tiles 243 and 288; two matrices: 210 tiles 60 and 48, 504 tiles 76 and 91,
+// 693 tiles 103 and 137, 1584 tiles 392 and 529.  (Tiles are counted with one of each
+// expert's that may be missing: 512 of 64 experts with 64 rows each 69 and 57.)
 constexpr int64_t kF32Blocks = 512;
 
 template <int NB, bool A_KC, bool B_KC, int EPI>
