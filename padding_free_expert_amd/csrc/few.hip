@@ -73,7 +73,7 @@ constexpr int kFewBlocks = 512, kBlocks = 1536;
 constexpr int kGateParts = 16;    // of the gate's sums: what the top-k reads for each logit
 constexpr int kPartRows = 16;     // see make_plan
 // Strips (times parts) from which each is a wave's own (see few_down_kernel): 64 tokens of 64
-// bf16 experts, 3072 of them, 207 us so and 215 by blocks, 12 tokens of them 149 and 151.
+// bf16 experts, 1.5 times as many, 207 us so and 215 by blocks, 12 tokens of them 149, 151.
 constexpr int kManyStrips = 2048;
 // Tokens and slots whose top-k the up-projection's blocks find themselves: a wave for each
 // token, no launch (4.5 us) between the gate and the experts.
@@ -1065,8 +1065,8 @@ Plan make_plan(const FewSizes &z, char *ws) {
     }
     // Launches with more strips than the compute units' waves take at once: a wave a strip,
     // and several of them a block, whose activations are formed once for all.  Two strips a
-    // wave from 8192 on, within 5% of one strip on either side (3072 of bf16 207 us with
-    // one, 212 with two; 6144 of 8 bits 128 and 122; 14336 255 and 257; 114688 1686 and 1673)
+    // wave from 8192 on, within 5% of one strip on either side (a third of that in bf16 207
+    // us with one, 212 with two; 6144 of 8 bits 128 and 122; 14336 255 and 257; 114688 1686 and 1673)
     const int64_t strips = pl.down + pl.down_shared;
     pl.wave_strips = strips >= kManyStrips;
     a.r.down_strips = pl.wave_strips ? kFewWaves * (strips >= 4 * kManyStrips ? 2 : 1) : 1;
